@@ -320,6 +320,128 @@ MEDUSA_API int medusa_tree_attention_noalloc(const medusa_cfg* cfg, const void* 
                                              const int32_t* L, const uint64_t* anc_bits, void* O,
                                              medusa_stream_t stream);
 
+/* Attention over whole prompts: what fills the cache that the step reads.
+ * "Speculative Decoding 원리와 가속 아키텍처" (blog.huny.dev), section 3, and
+ * "최적화 2편" (beengineer500), section 3.3 (block-wise softmax), describe decoding
+ * behind a prompt; the call itself has no counterpart on the pages.
+ * cfg->B prompts of different lengths lie packed one after another:
+ *   Q [T] rows of [Hq][D] elt, q_stride elements from row to row
+ *   K, V [T] rows of [Hkv][D] elt, k_stride and v_stride elements apart
+ *                              (so all three may be parts of one projection's output)
+ *   cu_rows [B+1] int32        sequence b owns rows [cu_rows[b], cu_rows[b+1])
+ *   O [T][Hq][D] elt, dense    row i of a sequence: softmax over its rows 0..i of
+ *                              q.k / sqrt(D), times v; KV head of query head h is
+ *                              h / (Hq / Hkv)
+ * Softmax and accumulation in float32; bf16 weights are rounded to bf16 before
+ * the product with V. Rows of O that no sequence owns are left as they are.
+ * cu_rows must not decrease; a sequence with cu_rows[b] < 0, cu_rows[b+1] <
+ * cu_rows[b] or cu_rows[b+1] > T is skipped. Non-finite values stay within
+ * their own sequence. O must not overlap Q, K or V. T = 0 enqueues nothing.
+ * From cfg only B, Hq, Hkv, D and dtype are used (every prompt length is
+ * allowed, whatever L_cap). Q, K, V, O 16-byte aligned; strides multiples of 16
+ * bytes and at least Hq * D (Hkv * D): MEDUSA_ERR_INVALID_ARG otherwise. Needs
+ * no workspace. */
+MEDUSA_API int medusa_prompt_attention(const medusa_cfg* cfg, const void* Q, const void* K, const void* V, int32_t T,
+                                       int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t* cu_rows,
+                                       void* O, medusa_stream_t stream);
+
+/* A prompt's keys and values (one layer's) into the pages of a cache.
+ *   K, V, T, k_stride, v_stride, cu_rows   as for medusa_prompt_attention
+ *   start [B] int32            logical row that sequence b's row 0 becomes; NULL: 0
+ *   Kp, Vp, num_pages, page_rows, block_table   as for medusa_tree_attention_paged
+ *                              (any dtype and D)
+ * Row r of sequence b goes to logical row start[b] + r, in every KV head. A row
+ * outside [0, L_cap), or whose block-table page id lies outside [0, num_pages),
+ * is not written; lengths are the caller's to set. Sequences that write must own
+ * their pages (forked sequences share whole pages: the rows stored in one are
+ * every holder's). T = 0 enqueues nothing. */
+MEDUSA_API int medusa_kv_store_paged(const medusa_cfg* cfg, const void* K, const void* V, int32_t T, int64_t k_stride,
+                                     int64_t v_stride, const int32_t* cu_rows, const int32_t* start, void* Kp, void* Vp,
+                                     int32_t num_pages, int32_t page_rows, const int32_t* block_table,
+                                     medusa_stream_t stream);
+
+/* Tree attention of a batch whose sequences share a long prefix, read once for
+ * all of them. Arguments and results are those of medusa_tree_attention_paged,
+ * with the logical rows [0, shared_rows) of EVERY sequence taken from the pages
+ *   prefix_table [ceil(shared_rows / page_rows)] int32
+ * (for example the first entries of a forked sequence's block-table row) instead
+ * of its own block-table row, whose entries for those rows are not read, except
+ * that rows from shared_rows on in a page that holds both come from the
+ * sequence's own entry. A sequence with L_b < shared_rows attends to the first
+ * L_b of them. shared_rows: a multiple of 128 in [0, L_cap] (MEDUSA_ERR_UNSUPPORTED
+ * otherwise); 0 shares nothing and prefix_table may be NULL. A single token per
+ * sequence is a tree of one node (cfg->tree_nodes = 1). All query rows that share
+ * a KV head meet each tile of the prefix together; the rest is attended per
+ * sequence; the partial results merge by their maxima and exp-sums ("최적화 2편"
+ * (beengineer500), section 3.3). A row of the cache past L_b never reaches a
+ * result, whatever it holds. bf16 with D = 128 only (MEDUSA_ERR_UNSUPPORTED
+ * otherwise). The workspace has medusa_prefix_workspace_size() bytes (256-byte
+ * aligned); each call writes all of it that it reads. */
+MEDUSA_API int medusa_prefix_workspace_size(const medusa_cfg* cfg, int32_t shared_rows, size_t* bytes);
+MEDUSA_API int medusa_tree_attention_prefix(const medusa_cfg* cfg, const void* Q, const void* Kp, const void* Vp,
+                                            int32_t num_pages, int32_t page_rows, const int32_t* prefix_table,
+                                            int32_t shared_rows, const int32_t* block_table, const void* Kt,
+                                            const void* Vt, const int32_t* L, const uint64_t* anc_bits, void* O,
+                                            void* workspace, medusa_stream_t stream);
+
+/* Pages of a cache: who holds them, on the device.
+ *   block_table [B][L_cap / page_rows] int32   page ids; a negative entry holds no page
+ *   refs [num_pages] int32                     how many block-table entries hold a page
+ *                                              (0: the page is free)
+ *   L [B] int32                                committed lengths
+ *   Kp, Vp, n_layers, pool_layer_elems         every layer's pool, as for
+ *                                              medusa_kv_commit_paged, with num_pages
+ *                                              pages in each
+ * page_rows as for medusa_tree_attention_paged; any dtype and D. The caller
+ * starts with block_table = -1, refs = 0 and L = 0. Every result is
+ * deterministic: new pages are the free pages of the lowest ids, in order.
+ * workspace: medusa_pages_workspace_size() bytes, 256-byte aligned; each call
+ * writes all of it that it reads. Two calls on the same tables must be ordered
+ * (one stream does that). */
+MEDUSA_API int medusa_pages_workspace_size(const medusa_cfg* cfg, int32_t num_pages, size_t* bytes);
+
+/* Pages for rows [B] int32 logical rows of each sequence: every negative entry
+ * among the first ceil(rows[b] / page_rows) of its row gets a free page
+ * (refs = 1); others stay. flags [B] uint32 is overwritten with 0 or
+ * MEDUSA_FLAG_CAPACITY: rows[b] lies outside [0, L_cap], or the free pages do not
+ * suffice for the sequences up to b together; such a sequence stays as it is. */
+MEDUSA_API int medusa_pages_reserve(const medusa_cfg* cfg, int32_t num_pages, int32_t page_rows, const int32_t* rows,
+                                    int32_t* block_table, int32_t* refs, uint32_t* flags, void* workspace,
+                                    medusa_stream_t stream);
+
+/* n forks (0 <= n <= B): sequence dst[i] becomes a continuation of src[i]
+ * (src, dst [n] int32). It shares src's full pages (refs + 1 each); the first
+ * L_src mod page_rows rows of a partly filled last page are copied, in every
+ * layer, to a free page of its own; L[dst] = L[src]. Pages that src holds beyond
+ * its length are not passed on. The same src may come several times.
+ * flags [n] uint32 is overwritten with 0, or with the reason why fork i changed
+ * nothing: MEDUSA_FLAG_PAGES when an index lies outside [0, B), L_src outside
+ * [0, L_cap], a page id that src needs outside [0, num_pages), or dst[i] holds a
+ * page, is some fork's src, or is another fork's dst; MEDUSA_FLAG_CAPACITY when
+ * the free pages do not suffice for the forks up to i together. */
+#define MEDUSA_FLAG_PAGES 16u /* an index or a table that a page operation cannot act on */
+MEDUSA_API int medusa_pages_fork(const medusa_cfg* cfg, void* Kp, void* Vp, int32_t num_pages, int32_t page_rows,
+                                 int32_t n_layers, size_t pool_layer_elems, int32_t n, const int32_t* src,
+                                 const int32_t* dst, int32_t* block_table, int32_t* L, int32_t* refs, uint32_t* flags,
+                                 void* workspace, medusa_stream_t stream);
+
+/* Frees n sequences (seqs [n] int32, n >= 0): each page that one of them holds
+ * loses a reference, the entries become -1 and L 0. A sequence named twice is
+ * freed once; an index outside [0, B) is passed over. */
+MEDUSA_API int medusa_pages_free(const medusa_cfg* cfg, int32_t num_pages, int32_t page_rows, int32_t n,
+                                 const int32_t* seqs, int32_t* block_table, int32_t* L, int32_t* refs,
+                                 medusa_stream_t stream);
+
+/* Moves the pages in use to the front of every layer's pool: with n_live pages
+ * in use, those with an id >= n_live move, in order, to the free ids below
+ * n_live. Block-table entries and refs follow; page_map [num_pages] int32
+ * receives each page's new id (-1: it was free), for tables the caller keeps
+ * elsewhere, and n_live [1] int32 their number. An entry that holds a page
+ * without references becomes -1; ids outside [0, num_pages) stay as they are. */
+MEDUSA_API int medusa_pages_compact(const medusa_cfg* cfg, void* Kp, void* Vp, int32_t num_pages, int32_t page_rows,
+                                    int32_t n_layers, size_t pool_layer_elems, int32_t* block_table, int32_t* refs,
+                                    int32_t* page_map, int32_t* n_live, void* workspace, medusa_stream_t stream);
+
 /* Failure detection. Every spin-wait of the tcgen05 kernels (the heads GEMVs and
  * tree attention: pipeline mbarriers, the softmax exchanges) is bounded by a
  * clock budget of about two seconds. On expiry the waiting thread ORs a code

@@ -19,13 +19,16 @@ LIB_CHECKED_PATH = os.path.join(PKG, "libmedusa_checked.so")
 
 F32, BF16 = 0, 1
 GREEDY, REJECTION = 0, 1
-FLAG_RS_NEAR_TIE, FLAG_CDF_NEAR_TIE, FLAG_CAPACITY = 1, 2, 4
+FLAG_RS_NEAR_TIE, FLAG_CDF_NEAR_TIE, FLAG_CAPACITY, FLAG_PAGES = 1, 2, 4, 16
 
 ENTRY_POINTS = ("medusa_node_count", "medusa_workspace_size", "medusa_heads", "medusa_tree_build",
                 "medusa_tree_attention", "medusa_verify", "medusa_kv_compact", "medusa_tree_attention_noalloc",
                 "medusa_tree_attention_paged", "medusa_kv_commit_paged", "medusa_step_graph_create",
                 "medusa_step_graph_launch", "medusa_step_graph_destroy", "medusa_poll_errors",
                 "medusa_selftest_wait_timeout", "medusa_checked_build", "medusa_poll_checks", "medusa_step_fused",
+                "medusa_prompt_attention", "medusa_kv_store_paged", "medusa_prefix_workspace_size",
+                "medusa_tree_attention_prefix", "medusa_pages_workspace_size", "medusa_pages_reserve",
+                "medusa_pages_fork", "medusa_pages_free", "medusa_pages_compact",
                 "medusa_launch_count", "medusa_status_string")
 CHECK_TOKEN, CHECK_TREE, CHECK_PATH, CHECK_PAGE = 1, 2, 4, 8
 
@@ -91,6 +94,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         raise RuntimeError(f"libmedusa not built: {path} is missing (run __graft_entry__.build())")
     lib = ctypes.CDLL(path)
     cp = ctypes.POINTER(Cfg)
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
     sig = {
         "medusa_node_count": [cp, ctypes.POINTER(ctypes.c_int32)],
         "medusa_workspace_size": [cp, ctypes.POINTER(ctypes.c_size_t)],
@@ -111,6 +115,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "medusa_checked_build": [],
         "medusa_step_fused": [cp, ctypes.POINTER(StepArgs), P],
         "medusa_poll_checks": [P, ctypes.POINTER(ctypes.c_uint32)],
+        "medusa_prompt_attention": [cp, P, P, P, i32, i64, i64, i64, P, P, P],
+        "medusa_kv_store_paged": [cp, P, P, i32, i64, i64, P, P, P, P, i32, i32, P, P],
+        "medusa_prefix_workspace_size": [cp, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "medusa_tree_attention_prefix": [cp, P, P, P, i32, i32, P, i32, P, P, P, P, P, P, P, P],
+        "medusa_pages_workspace_size": [cp, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "medusa_pages_reserve": [cp, i32, i32, P, P, P, P, P, P],
+        "medusa_pages_fork": [cp, P, P, i32, i32, i32, ctypes.c_size_t, i32, P, P, P, P, P, P, P, P],
+        "medusa_pages_free": [cp, i32, i32, i32, P, P, P, P, P],
+        "medusa_pages_compact": [cp, P, P, i32, i32, i32, ctypes.c_size_t, P, P, P, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -297,6 +310,75 @@ def verify(cfg, tokens, parent, first_child, target_logits, head_logits, u_acc, 
 def kv_compact(cfg, Kc, Vc, L, acc, path, kv_map, stream=None):
     _check("medusa_kv_compact", load().medusa_kv_compact(
         ctypes.byref(cfg), _ptr(Kc), _ptr(Vc), _ptr(L), _ptr(acc), _ptr(path), _ptr(kv_map), _stream(stream)))
+
+
+def prompt_attention(cfg, Q, K, V, T, q_stride, k_stride, v_stride, cu_rows, O, stream=None):
+    """Causal attention of the packed prompts of a batch; strides in elements from row to row."""
+    _check("medusa_prompt_attention", load().medusa_prompt_attention(
+        ctypes.byref(cfg), _ptr(Q), _ptr(K), _ptr(V), int(T), int(q_stride), int(k_stride), int(v_stride), _ptr(cu_rows),
+        _ptr(O), _stream(stream)))
+
+
+def kv_store_paged(cfg, K, V, T, k_stride, v_stride, cu_rows, start, Kp, Vp, num_pages, page_rows, block_table,
+                   stream=None):
+    """One layer's packed keys and values into the pages of their sequences; ``start`` may be None (0)."""
+    _check("medusa_kv_store_paged", load().medusa_kv_store_paged(
+        ctypes.byref(cfg), _ptr(K), _ptr(V), int(T), int(k_stride), int(v_stride), _ptr(cu_rows), _ptr(start), _ptr(Kp),
+        _ptr(Vp), int(num_pages), int(page_rows), _ptr(block_table), _stream(stream)))
+
+
+def prefix_workspace_size(cfg, shared_rows: int) -> int:
+    n = ctypes.c_size_t()
+    _check("medusa_prefix_workspace_size", load().medusa_prefix_workspace_size(ctypes.byref(cfg), int(shared_rows),
+                                                                                 ctypes.byref(n)))
+    return n.value
+
+
+def tree_attention_prefix(cfg, Q, Kp, Vp, num_pages, page_rows, prefix_table, shared_rows, block_table, Kt, Vt, L,
+                          anc_bits, O, workspace, stream=None):
+    """medusa_tree_attention_paged with the first ``shared_rows`` rows read once for the whole batch."""
+    _check("medusa_tree_attention_prefix", load().medusa_tree_attention_prefix(
+        ctypes.byref(cfg), _ptr(Q), _ptr(Kp), _ptr(Vp), int(num_pages), int(page_rows), _ptr(prefix_table),
+        int(shared_rows), _ptr(block_table), _ptr(Kt), _ptr(Vt), _ptr(L), _ptr(anc_bits), _ptr(O), _ptr(workspace),
+        _stream(stream)))
+
+
+def pages_workspace_size(cfg, num_pages: int) -> int:
+    n = ctypes.c_size_t()
+    _check("medusa_pages_workspace_size", load().medusa_pages_workspace_size(ctypes.byref(cfg), int(num_pages),
+                                                                               ctypes.byref(n)))
+    return n.value
+
+
+def pages_reserve(cfg, num_pages, page_rows, rows, block_table, refs, flags, workspace, stream=None):
+    """Free pages for ``rows[b]`` logical rows of every sequence."""
+    _check("medusa_pages_reserve", load().medusa_pages_reserve(
+        ctypes.byref(cfg), int(num_pages), int(page_rows), _ptr(rows), _ptr(block_table), _ptr(refs), _ptr(flags),
+        _ptr(workspace), _stream(stream)))
+
+
+def pages_fork(cfg, Kp, Vp, num_pages, page_rows, n_layers, pool_layer_elems, n, src, dst, block_table, L, refs, flags,
+               workspace, stream=None):
+    """Sequences ``dst`` continue sequences ``src``: full pages shared, the partly filled last page copied."""
+    _check("medusa_pages_fork", load().medusa_pages_fork(
+        ctypes.byref(cfg), _ptr(Kp), _ptr(Vp), int(num_pages), int(page_rows), int(n_layers), int(pool_layer_elems),
+        int(n), _ptr(src), _ptr(dst), _ptr(block_table), _ptr(L), _ptr(refs), _ptr(flags), _ptr(workspace),
+        _stream(stream)))
+
+
+def pages_free(cfg, num_pages, page_rows, n, seqs, block_table, L, refs, stream=None):
+    """The sequences ``seqs`` let go of their pages."""
+    _check("medusa_pages_free", load().medusa_pages_free(
+        ctypes.byref(cfg), int(num_pages), int(page_rows), int(n), _ptr(seqs), _ptr(block_table), _ptr(L), _ptr(refs),
+        _stream(stream)))
+
+
+def pages_compact(cfg, Kp, Vp, num_pages, page_rows, n_layers, pool_layer_elems, block_table, refs, page_map, n_live,
+                  workspace, stream=None):
+    """The pages in use move to the front of every layer's pool; tables and counts follow."""
+    _check("medusa_pages_compact", load().medusa_pages_compact(
+        ctypes.byref(cfg), _ptr(Kp), _ptr(Vp), int(num_pages), int(page_rows), int(n_layers), int(pool_layer_elems),
+        _ptr(block_table), _ptr(refs), _ptr(page_map), _ptr(n_live), _ptr(workspace), _stream(stream)))
 
 
 def raw_call(name: str, *args) -> int:

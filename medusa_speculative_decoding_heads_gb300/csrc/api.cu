@@ -62,6 +62,41 @@ int check_cfg(const medusa_cfg* c) {
   return MEDUSA_OK;
 }
 
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+int elts_per16(const medusa_cfg& c) { return c.dtype == MEDUSA_F32 ? 4 : 8; }
+
+// A packed row's stride: whole 16-byte words, and room for its heads.
+bool row_stride_ok(const medusa_cfg& c, int64_t stride, int heads) {
+  return stride >= (int64_t)heads * c.D && stride % elts_per16(c) == 0;
+}
+
+// Page geometry of the calls over a paged cache.
+int check_pages(const medusa_cfg& c, int num_pages, int page_rows) {
+  if (num_pages < 1) return MEDUSA_ERR_INVALID_ARG;
+  if (page_rows < 128 || page_rows % 128 != 0 || c.L_cap % page_rows != 0) return MEDUSA_ERR_UNSUPPORTED;
+  if ((int64_t)c.B * (c.L_cap / page_rows) > INT32_MAX) return MEDUSA_ERR_UNSUPPORTED;
+  return MEDUSA_OK;
+}
+
+// Every layer's pools: aligned, and with room for num_pages pages between two layers.
+int check_pools(const medusa_cfg& c, const void* Kp, const void* Vp, int num_pages, int page_rows, int n_layers,
+                size_t pool_layer_elems) {
+  if (!Kp || !Vp || n_layers < 1 || !aligned16(Kp) || !aligned16(Vp)) return MEDUSA_ERR_INVALID_ARG;
+  if (n_layers > 1 && (pool_layer_elems % elts_per16(c) != 0 ||
+                       pool_layer_elems < (size_t)num_pages * c.Hkv * page_rows * c.D))
+    return MEDUSA_ERR_INVALID_ARG;
+  if ((int64_t)c.Hkv * page_rows * c.D > INT32_MAX) return MEDUSA_ERR_UNSUPPORTED;
+  return MEDUSA_OK;
+}
+
+int check_prefix(const medusa_cfg& c, int shared_rows) {
+  if (shared_rows < 0) return MEDUSA_ERR_INVALID_ARG;
+  if (c.dtype != MEDUSA_BF16 || c.D != 128) return MEDUSA_ERR_UNSUPPORTED;
+  if (shared_rows % 128 != 0 || shared_rows > c.L_cap) return MEDUSA_ERR_UNSUPPORTED;
+  return MEDUSA_OK;
+}
+
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? MEDUSA_OK : MEDUSA_ERR_CUDA; }
 
 }  // namespace
@@ -210,6 +245,120 @@ int medusa_kv_commit_paged(const medusa_cfg* cfg, void* Kp, void* Vp, int32_t pa
                                           kv_map, (cudaStream_t)stream));
 }
 
+int medusa_prompt_attention(const medusa_cfg* cfg, const void* Q, const void* K, const void* V, int32_t T,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t* cu_rows, void* O,
+                            medusa_stream_t stream) {
+  int s = check_cfg(cfg);
+  if (s != MEDUSA_OK) return s;
+  if (T < 0) return MEDUSA_ERR_INVALID_ARG;
+  if (T == 0) return MEDUSA_OK;
+  if (!Q || !K || !V || !cu_rows || !O) return MEDUSA_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O)) return MEDUSA_ERR_INVALID_ARG;
+  if (!row_stride_ok(*cfg, q_stride, cfg->Hq) || !row_stride_ok(*cfg, k_stride, cfg->Hkv) ||
+      !row_stride_ok(*cfg, v_stride, cfg->Hkv))
+    return MEDUSA_ERR_INVALID_ARG;
+  return from_cuda(launch_prompt_attention(*cfg, Q, K, V, T, q_stride, k_stride, v_stride, cu_rows, O,
+                                           (cudaStream_t)stream));
+}
+
+int medusa_kv_store_paged(const medusa_cfg* cfg, const void* K, const void* V, int32_t T, int64_t k_stride,
+                          int64_t v_stride, const int32_t* cu_rows, const int32_t* start, void* Kp, void* Vp,
+                          int32_t num_pages, int32_t page_rows, const int32_t* block_table, medusa_stream_t stream) {
+  int s = check_cfg(cfg);
+  if (s == MEDUSA_OK) s = check_pages(*cfg, num_pages, page_rows);
+  if (s != MEDUSA_OK) return s;
+  if (T < 0) return MEDUSA_ERR_INVALID_ARG;
+  if (T == 0) return MEDUSA_OK;
+  if (!K || !V || !cu_rows || !Kp || !Vp || !block_table) return MEDUSA_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V) || !aligned16(Kp) || !aligned16(Vp)) return MEDUSA_ERR_INVALID_ARG;
+  if (!row_stride_ok(*cfg, k_stride, cfg->Hkv) || !row_stride_ok(*cfg, v_stride, cfg->Hkv)) return MEDUSA_ERR_INVALID_ARG;
+  return from_cuda(launch_kv_store_paged(*cfg, K, V, T, k_stride, v_stride, cu_rows, start, Kp, Vp, num_pages, page_rows,
+                                         block_table, (cudaStream_t)stream));
+}
+
+int medusa_prefix_workspace_size(const medusa_cfg* cfg, int32_t shared_rows, size_t* bytes) {
+  int s = check_cfg(cfg);
+  if (s == MEDUSA_OK) s = check_prefix(*cfg, shared_rows);
+  if (s != MEDUSA_OK) return s;
+  if (!bytes) return MEDUSA_ERR_INVALID_ARG;
+  *bytes = prefix_workspace(*cfg, shared_rows);
+  return MEDUSA_OK;
+}
+
+int medusa_tree_attention_prefix(const medusa_cfg* cfg, const void* Q, const void* Kp, const void* Vp, int32_t num_pages,
+                                 int32_t page_rows, const int32_t* prefix_table, int32_t shared_rows,
+                                 const int32_t* block_table, const void* Kt, const void* Vt, const int32_t* L,
+                                 const uint64_t* anc_bits, void* O, void* workspace, medusa_stream_t stream) {
+  int s = check_cfg(cfg);
+  if (s == MEDUSA_OK) s = check_pages(*cfg, num_pages, page_rows);
+  if (s == MEDUSA_OK) s = check_prefix(*cfg, shared_rows);
+  if (s != MEDUSA_OK) return s;
+  if (!Q || !Kp || !Vp || !block_table || !Kt || !Vt || !L || !anc_bits || !O || !workspace ||
+      (shared_rows > 0 && !prefix_table))
+    return MEDUSA_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(Kp) || !aligned16(Vp) || !aligned16(Kt) || !aligned16(Vt) || !aligned16(O))
+    return MEDUSA_ERR_INVALID_ARG;
+  if (!aligned256(workspace)) return MEDUSA_ERR_INVALID_ARG;
+  return from_cuda(launch_prefix_attention(*cfg, Q, Kp, Vp, num_pages, page_rows, prefix_table, shared_rows, block_table, Kt,
+                                           Vt, L, anc_bits, O, workspace, (cudaStream_t)stream));
+}
+
+int medusa_pages_workspace_size(const medusa_cfg* cfg, int32_t num_pages, size_t* bytes) {
+  int s = check_cfg(cfg);
+  if (s != MEDUSA_OK) return s;
+  if (!bytes || num_pages < 1) return MEDUSA_ERR_INVALID_ARG;
+  *bytes = pages_workspace(*cfg, num_pages);
+  return MEDUSA_OK;
+}
+
+int medusa_pages_reserve(const medusa_cfg* cfg, int32_t num_pages, int32_t page_rows, const int32_t* rows,
+                         int32_t* block_table, int32_t* refs, uint32_t* flags, void* workspace, medusa_stream_t stream) {
+  int s = check_cfg(cfg);
+  if (s == MEDUSA_OK) s = check_pages(*cfg, num_pages, page_rows);
+  if (s != MEDUSA_OK) return s;
+  if (!rows || !block_table || !refs || !flags || !workspace || !aligned256(workspace)) return MEDUSA_ERR_INVALID_ARG;
+  return from_cuda(launch_pages_reserve(*cfg, num_pages, page_rows, rows, block_table, refs, flags, workspace,
+                                        (cudaStream_t)stream));
+}
+
+int medusa_pages_fork(const medusa_cfg* cfg, void* Kp, void* Vp, int32_t num_pages, int32_t page_rows, int32_t n_layers,
+                      size_t pool_layer_elems, int32_t n, const int32_t* src, const int32_t* dst, int32_t* block_table,
+                      int32_t* L, int32_t* refs, uint32_t* flags, void* workspace, medusa_stream_t stream) {
+  int s = check_cfg(cfg);
+  if (s == MEDUSA_OK) s = check_pages(*cfg, num_pages, page_rows);
+  if (s == MEDUSA_OK) s = check_pools(*cfg, Kp, Vp, num_pages, page_rows, n_layers, pool_layer_elems);
+  if (s != MEDUSA_OK) return s;
+  if (n < 0 || n > cfg->B) return MEDUSA_ERR_INVALID_ARG;
+  if (n == 0) return MEDUSA_OK;
+  if (!src || !dst || !block_table || !L || !refs || !flags || !workspace || !aligned256(workspace))
+    return MEDUSA_ERR_INVALID_ARG;
+  return from_cuda(launch_pages_fork(*cfg, Kp, Vp, num_pages, page_rows, n_layers, pool_layer_elems, n, src, dst, block_table,
+                                     L, refs, flags, workspace, (cudaStream_t)stream));
+}
+
+int medusa_pages_free(const medusa_cfg* cfg, int32_t num_pages, int32_t page_rows, int32_t n, const int32_t* seqs,
+                      int32_t* block_table, int32_t* L, int32_t* refs, medusa_stream_t stream) {
+  int s = check_cfg(cfg);
+  if (s == MEDUSA_OK) s = check_pages(*cfg, num_pages, page_rows);
+  if (s != MEDUSA_OK) return s;
+  if (n < 0) return MEDUSA_ERR_INVALID_ARG;
+  if (n == 0) return MEDUSA_OK;
+  if (!seqs || !block_table || !L || !refs) return MEDUSA_ERR_INVALID_ARG;
+  return from_cuda(launch_pages_free(*cfg, num_pages, page_rows, n, seqs, block_table, L, refs, (cudaStream_t)stream));
+}
+
+int medusa_pages_compact(const medusa_cfg* cfg, void* Kp, void* Vp, int32_t num_pages, int32_t page_rows,
+                         int32_t n_layers, size_t pool_layer_elems, int32_t* block_table, int32_t* refs,
+                         int32_t* page_map, int32_t* n_live, void* workspace, medusa_stream_t stream) {
+  int s = check_cfg(cfg);
+  if (s == MEDUSA_OK) s = check_pages(*cfg, num_pages, page_rows);
+  if (s == MEDUSA_OK) s = check_pools(*cfg, Kp, Vp, num_pages, page_rows, n_layers, pool_layer_elems);
+  if (s != MEDUSA_OK) return s;
+  if (!block_table || !refs || !page_map || !n_live || !workspace || !aligned256(workspace)) return MEDUSA_ERR_INVALID_ARG;
+  return from_cuda(launch_pages_compact(*cfg, Kp, Vp, num_pages, page_rows, n_layers, pool_layer_elems, block_table, refs,
+                                        page_map, n_live, workspace, (cudaStream_t)stream));
+}
+
 }  // extern "C"
 
 struct medusa_step_graph {
@@ -319,14 +468,15 @@ int medusa_checked_build(void) {
 
 int medusa_poll_checks(medusa_stream_t stream, uint32_t* codes) {
   cudaStream_t st = (cudaStream_t)stream;
-  uint32_t w[4] = {0, 0, 0, 0};
+  uint32_t w[5] = {0, 0, 0, 0, 0};
   cudaError_t e = tree_take_checks(&w[0], st);
   if (e == cudaSuccess) e = verify_take_checks(&w[1], st);
   if (e == cudaSuccess) e = compact_take_checks(&w[2], st);
   if (e == cudaSuccess) e = attention_tc_take_checks(&w[3], st);
+  if (e == cudaSuccess) e = pages_take_checks(&w[4], st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return MEDUSA_ERR_CUDA;
-  const uint32_t all = w[0] | w[1] | w[2] | w[3];
+  const uint32_t all = w[0] | w[1] | w[2] | w[3] | w[4];
   if (codes) *codes = all;
   return all ? MEDUSA_ERR_BOUNDS : MEDUSA_OK;
 }

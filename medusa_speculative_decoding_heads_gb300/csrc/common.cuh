@@ -167,6 +167,31 @@ size_t verify_workspace(const medusa_cfg& c);
 cudaError_t launch_kv_compact(const medusa_cfg& c, void* Kc, void* Vc, int32_t* L, const int32_t* acc,
                               const int32_t* path, int32_t* kv_map, cudaStream_t st);
 
+// Attention over packed prompts, and tree attention behind a shared prefix (prompt.cu).
+cudaError_t launch_prompt_attention(const medusa_cfg& c, const void* Q, const void* K, const void* V, int T, int64_t q_stride,
+                                    int64_t k_stride, int64_t v_stride, const int32_t* cu, void* O, cudaStream_t st);
+size_t prefix_workspace(const medusa_cfg& c, int shared);
+cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const void* Kp, const void* Vp, int num_pages,
+                                    int page_rows, const int32_t* prefix, int shared, const int32_t* table, const void* Kt,
+                                    const void* Vt, const int32_t* L, const uint64_t* bits, void* O, void* ws,
+                                    cudaStream_t st);
+
+// Pages of a cache (pages.cu).
+size_t pages_workspace(const medusa_cfg& c, int num_pages);
+cudaError_t launch_pages_reserve(const medusa_cfg& c, int num_pages, int page_rows, const int32_t* rows, int32_t* table,
+                                 int32_t* refs, uint32_t* flags, void* ws, cudaStream_t st);
+cudaError_t launch_pages_fork(const medusa_cfg& c, void* Kp, void* Vp, int num_pages, int page_rows, int n_layers,
+                              size_t pool_layer_elems, int n, const int32_t* src, const int32_t* dst, int32_t* table,
+                              int32_t* L, int32_t* refs, uint32_t* flags, void* ws, cudaStream_t st);
+cudaError_t launch_pages_free(const medusa_cfg& c, int num_pages, int page_rows, int n, const int32_t* seqs, int32_t* table,
+                              int32_t* L, int32_t* refs, cudaStream_t st);
+cudaError_t launch_pages_compact(const medusa_cfg& c, void* Kp, void* Vp, int num_pages, int page_rows, int n_layers,
+                                 size_t pool_layer_elems, int32_t* table, int32_t* refs, int32_t* page_map, int32_t* n_live,
+                                 void* ws, cudaStream_t st);
+cudaError_t launch_kv_store_paged(const medusa_cfg& c, const void* K, const void* V, int T, int64_t k_stride, int64_t v_stride,
+                                  const int32_t* cu, const int32_t* start, void* Kp, void* Vp, int num_pages, int page_rows,
+                                  const int32_t* table, cudaStream_t st);
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // The whole step as one persistent cooperative launch (fused.cu): small batches,
@@ -213,6 +238,7 @@ cudaError_t tree_take_checks(uint32_t* out, cudaStream_t st);
 cudaError_t verify_take_checks(uint32_t* out, cudaStream_t st);
 cudaError_t compact_take_checks(uint32_t* out, cudaStream_t st);
 cudaError_t attention_tc_take_checks(uint32_t* out, cudaStream_t st);
+cudaError_t pages_take_checks(uint32_t* out, cudaStream_t st);
 
 // Configuration checks shared by every entry point (MEDUSA_OK or an error status).
 int check_cfg_public(const medusa_cfg* c);

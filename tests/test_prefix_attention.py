@@ -1,0 +1,195 @@
+"""medusa_tree_attention_prefix: tree attention of a batch behind one shared prefix, against float64."""
+import ctypes
+
+import pytest
+import torch
+
+from medusa_speculative_decoding_heads_gb300 import _build, binding as mb
+from oracle import serving_oracle as SO
+
+from _helpers import gpu_ready
+from _serving import ancestor_bits, assert_within, cfg_for, i32, tolerance
+
+BF16 = torch.bfloat16
+
+
+class Case:
+    """A shuffled pool: `shared` rows in pages of their own, each sequence's rows behind them in its own pages."""
+
+    def __init__(self, L, shared, P, Hq, Hkv, branching, dev, seed=0, poison=False, L_cap=None):
+        gen = torch.Generator(device=dev).manual_seed(seed)
+        cpu = torch.Generator().manual_seed(seed)
+        self.mask, self.bits = ancestor_bits(branching, dev)
+        self.N, self.B, self.P, self.shared, self.dev = self.mask.shape[0], len(L), P, shared, dev
+        most = max([shared] + list(L)) + self.N
+        self.L_cap = L_cap or -(-most // P) * P
+        width = self.L_cap // P
+        first = -(-shared // P)
+        num = first + self.B * width + 2
+        ids = torch.randperm(num, generator=cpu).tolist()
+        self.num, self.prefix, at = num, ids[:first], first
+        self.table = []
+        for n in L:
+            row = [-1] * width
+            for i in range(shared // P, -(-min(max(n, 0), self.L_cap) // P)):
+                row[i], at = ids[at], at + 1
+            self.table.append(row)
+        rnd = lambda *s: torch.randn(s, generator=gen, device=dev).to(BF16)
+        self.Q = rnd(self.B, self.N, Hq, 128) * 2
+        self.Kp, self.Vp = rnd(num, Hkv, P, 128), rnd(num, Hkv, P, 128)
+        self.Kt, self.Vt = rnd(self.B, Hkv, self.N, 128), rnd(self.B, Hkv, self.N, 128)
+        if poison:   # whatever no sequence may read: pages in nobody's hands, rows past each length
+            used = torch.zeros((num, P), dtype=torch.bool, device=dev)
+            for i in range(shared):
+                used[self.prefix[i // P], i % P] = True
+            for b, n in enumerate(L):
+                for i in range(shared, max(n, 0)):
+                    if n + self.N <= self.L_cap:
+                        used[self.table[b][i // P], i % P] = True
+            bad = ~used
+            self.Kp.transpose(1, 2)[bad] = float("nan")
+            self.Vp.transpose(1, 2)[bad] = float("nan")
+        self.L, self.Hq, self.Hkv, self.branching = list(L), Hq, Hkv, branching
+        self.cfg = cfg_for(self.B, Hq, Hkv, 128, BF16, self.L_cap, branching)
+        self.ws = torch.full((max(mb.prefix_workspace_size(self.cfg, shared), 256),), 255, dtype=torch.uint8, device=dev)
+
+    def call(self, O=None, stream=None, shared=None):
+        O = torch.full_like(self.Q, 7.0) if O is None else O
+        if not hasattr(self, "dtable"):
+            self.dtable, self.dprefix, self.dL = i32(self.table, self.dev), i32(self.prefix, self.dev), i32(self.L, self.dev)
+        mb.tree_attention_prefix(self.cfg, self.Q, self.Kp, self.Vp, self.num, self.P,
+                                 self.dprefix if self.prefix else None, self.shared, self.dtable, self.Kt, self.Vt, self.dL,
+                                 self.bits, O, self.ws, stream)
+        return O
+
+    def check(self, O, what="prefix attention", rows=slice(None)):
+        ref, A, S = SO.prefix_attention(self.Q, self.Kp, self.Vp, self.P, self.prefix, self.shared, self.table, self.Kt,
+                                        self.Vt, self.L, self.mask, self.L_cap)
+        tol = tolerance(BF16, ref, A, S, max(max(self.L), 1) + self.N)
+        assert_within(O[rows], ref[rows], tol[rows], what)
+        assert mb.poll_errors() == (0, 0, 0)
+
+
+TREES = [(1,), (2, 2), (3, 2, 2), (4, 3, 2, 1), (5, 3, 2, 1, 1)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("branching", TREES, ids=str)
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (8, 2), (6, 1), (14, 2), (16, 1), (3, 1)])
+def test_trees_and_heads(branching, Hq, Hkv):
+    dev = gpu_ready()
+    c = Case([400, 256, 257, 511, 384], 256, 128, Hq, Hkv, branching, dev, seed=Hq, poison=True)
+    c.check(c.call())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P", [128, 256])
+@pytest.mark.parametrize("shared", [0, 128, 384, 1024])
+@pytest.mark.parametrize("branching", [(1,), (3, 2, 2), (4, 3, 2, 1)], ids=str)
+def test_lengths(shared, P, branching):
+    """Lengths below, at and past the shared rows, zero, and page borders on either side."""
+    dev = gpu_ready()
+    L = sorted({0, 1, 127, 128, 129, max(shared - 1, 0), shared, shared + 1, shared + 127, shared + 128, shared + 129,
+                shared + 300})
+    c = Case(L, shared, P, 8, 2, branching, dev, seed=shared + P, poison=True)
+    c.check(c.call())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("branching", [(1,), (4, 3, 2, 1)], ids=str)
+def test_invalid_sequences_get_zeros(branching):
+    """A negative length, and one without room for the tree: zeros, the others right."""
+    dev = gpu_ready()
+    c = Case([300, -1, 512, 260, -2 ** 31], 256, 128, 8, 2, branching, dev, seed=3, poison=True, L_cap=512)
+    O = c.call()
+    for b in (1, 2, 4):
+        assert bool((O[b] == 0).all()), b
+    c.check(O)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,branching,Hq,Hkv", [(1, (1,), 4, 4), (1, (4, 3, 2, 1), 8, 2), (33, (1,), 8, 1), (70, (2, 2), 4, 2)])
+def test_batches(B, branching, Hq, Hkv):
+    """One sequence (the prefix alone is split over the GPU) up to many; a prefix of thousands of rows."""
+    dev = gpu_ready()
+    L = [2048 + (37 * b) % 300 for b in range(B)]
+    c = Case(L, 2048, 256, Hq, Hkv, branching, dev, seed=B)
+    c.check(c.call())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("branching", [(1,), (4, 3, 2, 1)], ids=str)
+def test_page_ids_outside_the_pool(branching):
+    """A table entry outside the pool reads no memory outside it; the other sequences are right."""
+    dev = gpu_ready()
+    c = Case([400, 400, 400], 256, 128, 8, 2, branching, dev, seed=4)
+    c.table[1][2], c.table[1][3] = c.num + 5, -3
+    O = c.call()
+    c.table[1] = c.table[0]   # sequence 1 is not compared
+    for b in (0, 2):
+        c.check(O, rows=slice(b, b + 1))
+
+
+@pytest.mark.gpu
+def test_streams_graph_and_workspace():
+    """Two calls at once with workspaces of their own; a captured call replayed with other lengths;
+    two calls of different sizes that take turns with one workspace."""
+    dev = gpu_ready()
+    cs = [Case([300, 700, 256], 256, 128, 8, 2, (4, 3, 2, 1), dev, seed=s) for s in (1, 2)]
+    want = [c.call() for c in cs]
+    outs, streams = [torch.full_like(w, 7.0) for w in want], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for c, o, st in zip(cs, outs, streams):
+            c.call(o, st)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    c, O = cs[0], torch.full_like(want[0], 7.0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.call(O)
+    c.L = [256, 301, 100]
+    c.dL.copy_(i32(c.L, dev))
+    for _ in range(3):
+        g.replay()
+    c.check(O, "replayed")
+    small = Case([130], 128, 128, 8, 2, (1,), dev, seed=5)
+    small.ws = c.ws
+    for _ in range(2):
+        small.check(small.call(), "small call in the same workspace")
+        c.check(c.call(), "large call in the same workspace")
+
+
+# ----------------------------------------------------------------------------- refusals (no GPU)
+def status(num_pages=9, P=128, shared=256, L_cap=1024, dtype=BF16, D=128, drop=None, off=None):
+    _build.build()
+    cfg = cfg_for(2, 4, 2, D, dtype, L_cap)
+    at = {n: 4096 for n in ("Q", "Kp", "Vp", "prefix", "table", "Kt", "Vt", "L", "bits", "O", "ws")}
+    if drop:
+        at[drop] = 0
+    if off:
+        at[off] += 8
+    p = {n: ctypes.c_void_p(x) if x else None for n, x in at.items()}
+    return mb.load().medusa_tree_attention_prefix(ctypes.byref(cfg), p["Q"], p["Kp"], p["Vp"], num_pages, P, p["prefix"], shared,
+                                                  p["table"], p["Kt"], p["Vt"], p["L"], p["bits"], p["O"], p["ws"], None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    *[(dict(drop=n), -1) for n in ("Q", "Kp", "Vp", "prefix", "table", "Kt", "Vt", "L", "bits", "O", "ws")],
+    *[(dict(off=n), -1) for n in ("Q", "Kp", "Vp", "Kt", "Vt", "O", "ws")],
+    (dict(num_pages=0), -1), (dict(P=64), -2), (dict(P=192), -2), (dict(P=384), -2), (dict(shared=-128), -1),
+    (dict(shared=100), -2), (dict(shared=1152), -2), (dict(dtype=torch.float32), -2), (dict(D=64), -2),
+])
+def test_refusals(kw, want):
+    assert status(**kw) == want
+
+
+def test_workspace_size_refusals():
+    _build.build()
+    size = lambda cfg, s: mb.raw_call("medusa_prefix_workspace_size", ctypes.byref(cfg), s, ctypes.byref(ctypes.c_size_t()))
+    good = cfg_for(2, 4, 2, 128, BF16)
+    assert size(good, 256) == 0 and size(good, 0) == 0
+    assert size(good, 100) == -2 and size(good, -1) == -1 and size(good, 2048) == -2
+    assert size(cfg_for(2, 4, 2, 64, BF16), 256) == -2
+    assert mb.raw_call("medusa_prefix_workspace_size", ctypes.byref(good), 256, None) == -1
