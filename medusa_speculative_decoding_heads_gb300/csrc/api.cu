@@ -299,6 +299,9 @@ int medusa_tree_attention_prefix(const medusa_cfg* cfg, const void* Q, const voi
   if (!aligned16(Q) || !aligned16(Kp) || !aligned16(Vp) || !aligned16(Kt) || !aligned16(Vt) || !aligned16(O))
     return MEDUSA_ERR_INVALID_ARG;
   if (!aligned256(workspace)) return MEDUSA_ERR_INVALID_ARG;
+  // page planes and query rows are counted in 32 bits
+  if (((int64_t)num_pages + 1) * cfg->Hkv > INT32_MAX || (int64_t)cfg->B * tree_shape(*cfg).N * cfg->Hq > INT32_MAX)
+    return MEDUSA_ERR_UNSUPPORTED;
   return from_cuda(launch_prefix_attention(*cfg, Q, Kp, Vp, num_pages, page_rows, prefix_table, shared_rows, block_table, Kt,
                                            Vt, L, anc_bits, O, workspace, (cudaStream_t)stream));
 }
@@ -430,13 +433,14 @@ int medusa_step_graph_destroy(medusa_step_graph* g) {
 
 int medusa_poll_errors(medusa_stream_t stream, uint32_t* heads_codes, uint32_t* attention_codes) {
   cudaStream_t st = (cudaStream_t)stream;
-  uint32_t h = 0, a = 0, f = 0;
+  uint32_t h = 0, a = 0, f = 0, r = 0;
   cudaError_t e = heads_tc_take_error(&h, st);
   if (e == cudaSuccess) e = attention_tc_take_error(&a, st);
   if (e == cudaSuccess) e = fused_take_error(&f, st);
-  a |= f;
+  if (e == cudaSuccess) e = rows_tc_take_error(&r, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return MEDUSA_ERR_CUDA;
+  a |= f | r;
   if (heads_codes) *heads_codes = h;
   if (attention_codes) *attention_codes = a;
   return (h | a) ? MEDUSA_ERR_TIMEOUT : MEDUSA_OK;
@@ -468,15 +472,16 @@ int medusa_checked_build(void) {
 
 int medusa_poll_checks(medusa_stream_t stream, uint32_t* codes) {
   cudaStream_t st = (cudaStream_t)stream;
-  uint32_t w[5] = {0, 0, 0, 0, 0};
+  uint32_t w[6] = {0, 0, 0, 0, 0, 0};
   cudaError_t e = tree_take_checks(&w[0], st);
   if (e == cudaSuccess) e = verify_take_checks(&w[1], st);
   if (e == cudaSuccess) e = compact_take_checks(&w[2], st);
   if (e == cudaSuccess) e = attention_tc_take_checks(&w[3], st);
   if (e == cudaSuccess) e = pages_take_checks(&w[4], st);
+  if (e == cudaSuccess) e = rows_tc_take_checks(&w[5], st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return MEDUSA_ERR_CUDA;
-  const uint32_t all = w[0] | w[1] | w[2] | w[3] | w[4];
+  const uint32_t all = w[0] | w[1] | w[2] | w[3] | w[4] | w[5];
   if (codes) *codes = all;
   return all ? MEDUSA_ERR_BOUNDS : MEDUSA_OK;
 }

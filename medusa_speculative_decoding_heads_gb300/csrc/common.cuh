@@ -167,7 +167,11 @@ size_t verify_workspace(const medusa_cfg& c);
 cudaError_t launch_kv_compact(const medusa_cfg& c, void* Kc, void* Vc, int32_t* L, const int32_t* acc,
                               const int32_t* path, int32_t* kv_map, cudaStream_t st);
 
-// Attention over packed prompts, and tree attention behind a shared prefix (prompt.cu).
+// Attention over packed prompts (prompt.cu), its tcgen05 form and tree attention behind a shared
+// prefix (rows_tc.cu).
+cudaError_t launch_prompt_tc(const medusa_cfg& c, const void* Q, const void* K, const void* V, int T, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const int32_t* cu, void* O, cudaStream_t st);
+cudaError_t rows_tc_take_error(uint32_t* out, cudaStream_t st);
 cudaError_t launch_prompt_attention(const medusa_cfg& c, const void* Q, const void* K, const void* V, int T, int64_t q_stride,
                                     int64_t k_stride, int64_t v_stride, const int32_t* cu, void* O, cudaStream_t st);
 size_t prefix_workspace(const medusa_cfg& c, int shared);
@@ -239,6 +243,7 @@ cudaError_t verify_take_checks(uint32_t* out, cudaStream_t st);
 cudaError_t compact_take_checks(uint32_t* out, cudaStream_t st);
 cudaError_t attention_tc_take_checks(uint32_t* out, cudaStream_t st);
 cudaError_t pages_take_checks(uint32_t* out, cudaStream_t st);
+cudaError_t rows_tc_take_checks(uint32_t* out, cudaStream_t st);
 
 // Configuration checks shared by every entry point (MEDUSA_OK or an error status).
 int check_cfg_public(const medusa_cfg* c);

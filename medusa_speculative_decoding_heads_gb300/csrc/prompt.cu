@@ -1,5 +1,5 @@
-// Causal attention over packed prompts, and tree attention behind a shared prefix: one
-// warp per query row and head.
+// Causal attention over packed prompts: one warp per query row and head (float32, and bf16
+// with D = 64; bf16 with D = 128 takes the tcgen05 kernel of rows_tc.cu).
 //
 // O = softmax(q.k / sqrt(D)) v over the visible keys, 32 keys at a time: lane = key for
 // the scores, lane = head dim for the weighted sum of values, with the running maximum and
@@ -90,48 +90,6 @@ prompt_rows_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __
   r.store(O + ((size_t)t * Hq + h) * D);
 }
 
-__global__ void __launch_bounds__(kRowWarps * 32)
-prefix_rows_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ Kp, const uint16_t* __restrict__ Vp,
-                   int num_pages, int P, const int32_t* __restrict__ prefix, int S, const int32_t* __restrict__ table,
-                   int max_pages, const uint16_t* __restrict__ Kt, const uint16_t* __restrict__ Vt,
-                   const int32_t* __restrict__ L, const uint64_t* __restrict__ bits, int B, int N, int Hq, int Hkv,
-                   int L_cap, float scale_log2, uint16_t* __restrict__ O) {
-  constexpr int D = 128;
-  pdl_wait();
-  pdl_trigger();
-  const int64_t w = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int h = (int)(w % Hq), n = (int)((w / Hq) % N);
-  const int64_t b = w / ((int64_t)Hq * N);
-  if (b >= B) return;
-  const int kvh = h / (Hq / Hkv), Lb = L[b];
-  WarpRow<uint16_t, D> r;
-  const size_t at = (((size_t)b * N + n) * Hq + h) * D;
-  r.begin(Q + at, scale_log2);
-  if (Lb >= 0 && Lb + N <= L_cap) {
-    for (int k0 = 0; k0 < Lb; k0 += 32) {
-      const int key = k0 + lane;
-      const uint16_t *kp = nullptr, *vp = nullptr;
-      if (key < Lb) {
-        const int page = key < S ? prefix[key / P] : table[(size_t)b * max_pages + key / P];
-        if (page >= 0 && page < num_pages) {
-          const size_t row = ((size_t)page * Hkv + kvh) * P + key % P;
-          kp = Kp + row * D;
-          vp = Vp + row * D;
-        }
-      }
-      r.block(kp, vp);
-    }
-    for (int j0 = 0; j0 < N; j0 += 32) {
-      const int j = j0 + lane;
-      const bool see = j < N && ((bits[2 * n + (j >> 6)] >> (j & 63)) & 1ull);
-      const size_t row = (((size_t)b * Hkv + kvh) * N + j) * D;
-      r.block(see ? Kt + row : nullptr, see ? Vt + row : nullptr);
-    }
-  }
-  r.store(O + at);
-}
-
 template <typename T, int D>
 cudaError_t run_prompt(const medusa_cfg& c, const void* Q, const void* K, const void* V, int T_rows, int64_t qs, int64_t ks,
                        int64_t vs, const int32_t* cu, void* O, cudaStream_t st) {
@@ -146,30 +104,13 @@ cudaError_t run_prompt(const medusa_cfg& c, const void* Q, const void* K, const 
 
 cudaError_t launch_prompt_attention(const medusa_cfg& c, const void* Q, const void* K, const void* V, int T_rows, int64_t qs,
                                     int64_t ks, int64_t vs, const int32_t* cu, void* O, cudaStream_t st) {
+  if (c.dtype == MEDUSA_BF16 && c.D == 128) return launch_prompt_tc(c, Q, K, V, T_rows, qs, ks, vs, cu, O, st);
   cudaError_t e;
   if (c.dtype == MEDUSA_F32)
     e = c.D == 64 ? run_prompt<float, 64>(c, Q, K, V, T_rows, qs, ks, vs, cu, O, st)
                   : run_prompt<float, 128>(c, Q, K, V, T_rows, qs, ks, vs, cu, O, st);
   else
-    e = c.D == 64 ? run_prompt<uint16_t, 64>(c, Q, K, V, T_rows, qs, ks, vs, cu, O, st)
-                  : run_prompt<uint16_t, 128>(c, Q, K, V, T_rows, qs, ks, vs, cu, O, st);
-  note_launches(1);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-size_t prefix_workspace(const medusa_cfg&, int) { return 0; }
-
-cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const void* Kp, const void* Vp, int num_pages,
-                                    int page_rows, const int32_t* prefix, int shared, const int32_t* table, const void* Kt,
-                                    const void* Vt, const int32_t* L, const uint64_t* bits, void* O, void*, cudaStream_t st) {
-  const TreeShape ts = tree_shape(c);
-  const float scale_log2 = (float)(1.4426950408889634 / sqrt(128.0));
-  const int64_t warps = (int64_t)c.B * ts.N * c.Hq;
-  const cudaError_t e = launch_pdl(
-      prefix_rows_kernel, (unsigned)((warps + kRowWarps - 1) / kRowWarps), kRowWarps * 32, 0, st,
-      static_cast<const uint16_t*>(Q), static_cast<const uint16_t*>(Kp), static_cast<const uint16_t*>(Vp), num_pages,
-      page_rows, prefix, shared, table, c.L_cap / page_rows, static_cast<const uint16_t*>(Kt),
-      static_cast<const uint16_t*>(Vt), L, bits, c.B, ts.N, c.Hq, c.Hkv, c.L_cap, scale_log2, static_cast<uint16_t*>(O));
+    e = run_prompt<uint16_t, 64>(c, Q, K, V, T_rows, qs, ks, vs, cu, O, st);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
