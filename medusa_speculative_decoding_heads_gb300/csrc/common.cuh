@@ -167,13 +167,13 @@ size_t verify_workspace(const medusa_cfg& c);
 cudaError_t launch_kv_compact(const medusa_cfg& c, void* Kc, void* Vc, int32_t* L, const int32_t* acc,
                               const int32_t* path, int32_t* kv_map, cudaStream_t st);
 
-// Attention over packed prompts (prompt.cu), its tcgen05 form and tree attention behind a shared
-// prefix (rows_tc.cu).
+// Attention over packed prompts: bf16 on tcgen05 (rows_tc.cu, also tree attention behind a shared
+// prefix), float32 on the CUDA cores (prompt_f32.cu).
 cudaError_t launch_prompt_tc(const medusa_cfg& c, const void* Q, const void* K, const void* V, int T, int64_t q_stride,
                              int64_t k_stride, int64_t v_stride, const int32_t* cu, void* O, cudaStream_t st);
 cudaError_t rows_tc_take_error(uint32_t* out, cudaStream_t st);
-cudaError_t launch_prompt_attention(const medusa_cfg& c, const void* Q, const void* K, const void* V, int T, int64_t q_stride,
-                                    int64_t k_stride, int64_t v_stride, const int32_t* cu, void* O, cudaStream_t st);
+cudaError_t launch_prompt_f32(const medusa_cfg& c, const void* Q, const void* K, const void* V, int T, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, const int32_t* cu, void* O, cudaStream_t st);
 size_t prefix_workspace(const medusa_cfg& c, int shared);
 cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const void* Kp, const void* Vp, int num_pages,
                                     int page_rows, const int32_t* prefix, int shared, const int32_t* table, const void* Kt,

@@ -1,6 +1,6 @@
 // Attention of packed query rows on 5th-generation tensor cores (tcgen05, TMEM
-// accumulators, TMA), bf16 with D = 128: whole prompts (causal), and tree attention
-// behind a prefix that the batch shares.
+// accumulators, TMA), bf16: whole prompts (causal; D = 64 or 128), and tree attention
+// behind a prefix that the batch shares (D = 128).
 //
 // O = softmax(Q K^T / sqrt(D)) V in one pass over the keys, with the running maximum and
 // sum of "최적화 2편" (beengineer500), section 3.3. 4 rows keys D operations against
@@ -10,20 +10,21 @@
 // A unit of work is 256 query rows of one KV head (two tiles of 128) against a range of
 // keys. A tile's rows are Gp query heads of the KV head's group times 128 / Gp positions
 // (Gp: the largest power of two that divides the group, at most 16), so that one TMA box
-// loads it and the heads share every K/V tile. 12 warps, one CTA per SM, which walks
-// units u = blockIdx.x, + gridDim.x, ...:
+// loads it and the heads share every K/V tile. 12 warps, one CTA per SM, which takes
+// units round by round:
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1: thread = row = TMEM lane; S (f32) to
 //                   registers, mask, maximum, 2^(s - m) rounded to bf16 back over S, sums
 //                   in f32. O is rescaled only when the maximum rises by more than 2^8.
+//                   The product with V begins once half of the weights are there.
 //   warp 8          issues every MMA: S_t(j) = Q_t K_j^T (both operands in shared memory)
 //                   and O_t += P_t(j) V_j (P from TMEM), so that one tile's products run
 //                   while the other tile's softmax does. MMAs of one issuing thread run in
 //                   order: S_t(j + 1), which overwrites P_t(j), follows O_t += P_t(j) V_j.
 //   warp 9          TMA: Q tiles, then K and V tiles of 128 keys alternating through one
-//                   5-stage ring. V rows past the last key that may be read are zeroed in
+//                   ring of 160 KB. V rows past the last key that may be read are zeroed in
 //                   shared memory (0 x NaN must not reach a result).
 //   warp 10         the schedule: decodes the next unit while the others work on this one.
-// TMEM: S_0, S_1, O_0, O_1 (128 columns each). Every mbarrier wait is bounded.
+// TMEM: S_0, S_1, O_0, O_1 (128 columns each; O uses D of them). Every mbarrier wait is bounded.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -33,6 +34,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "prompt_walk.cuh"
 #include "tc_common.cuh"
 
 namespace medusa {
@@ -41,12 +43,16 @@ __device__ uint32_t g_rows_tc_error = 0;
 
 namespace {
 
-constexpr int kD = 128, kRows = 128, kKeys = 128;
-constexpr int kHalf = 128 * 128;            // 128 rows x 64 bf16, 128-byte swizzle: half a tile (16 KB)
-constexpr int kTile = 2 * kHalf;            // 128 x 128 bf16 (32 KB)
-constexpr int kStages = 5;                  // K/V ring
-constexpr int kOffRing = 2 * kTile;         // behind the two Q tiles
-constexpr int kSmem = kOffRing + kStages * kTile + 1024;   // + alignment slack
+constexpr int kRows = 128, kKeys = 128;
+constexpr int kHalf = 128 * 128;            // 128 rows x 64 bf16, 128-byte swizzle (16 KB): a tile of D = 64
+template <int D>
+struct Layout {
+  static constexpr int halves = D / 64;
+  static constexpr int tile = halves * kHalf;        // 128 x D bf16
+  static constexpr int stages = 160 * 1024 / tile;   // K/V ring
+  static constexpr int ring = 2 * tile;              // behind the two Q tiles
+  static constexpr int smem = ring + stages * tile + 1024;   // + alignment slack
+};
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
@@ -99,6 +105,56 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// mbarrier.test_wait: asks without being suspended.
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(ok)
+               : "r"(tc::saddr(b)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+// Bounded wait of the issuing thread: it polls, since being suspended and woken costs more than
+// the gaps that it has to fill.
+__device__ __forceinline__ bool mbar_poll(uint64_t* b, uint32_t parity, uint32_t* err, uint32_t code) {
+  if (mbar_test(b, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_test(b, parity)) {
+    if (clock64() - t0 > 4000000000LL) {
+      atomicOr(err, code);
+      return false;
+    }
+  }
+  return true;
+}
+// 32 columns of this warp's TMEM lanes, and the wait that makes them readable: the registers
+// pass through it, so that no use of them can be moved ahead of it.
+__device__ __forceinline__ void tmem_landed32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ float max32(const uint32_t* v) {
+  float m = __uint_as_float(v[0]);
+#pragma unroll
+  for (int x = 1; x < 31; x += 2) m = max3(m, __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+  return fmaxf(m, __uint_as_float(v[31]));
+}
+// p = 2^(s scale - m) of 32 scores as 16 bf16 pairs; their float32 values are added to acc.
+__device__ __forceinline__ void exp32(const uint32_t* v, float scale_log2, float neg_m, uint32_t* pk, float2* acc) {
+  const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(neg_m, neg_m);
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    const float2 e = __ffma2_rn(make_float2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1])), sc, nm);
+    float2 p;
+    p.x = tc::ex2(e.x);
+    p.y = tc::ex2(e.y);
+    acc[x & 1] = __fadd2_rn(acc[x & 1], p);
+    pk[x] = pack_bf16x2(p.x, p.y);
+  }
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -106,46 +162,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(tc::saddr(bar))
       : "memory");
 }
-
-// Walks the prompts' units, those with the most keys first: by tile number from the last one
-// down, then by sequence. A whole warp calls it; units must be asked for in ascending order.
-struct PromptWalk {
-  int t = -1, before = 0, count = 0;   // units of tile number t follow `before` earlier ones
-
-  static __device__ __forceinline__ int tiles(const RowsArgs& a, int b, int per) {
-    if (b >= a.B) return 0;
-    const int c0 = a.cu[b], c1 = a.cu[b + 1];
-    return (c0 >= 0 && c1 >= c0 && c1 <= a.T) ? (int)(((int64_t)(c1 - c0) + per - 1) / per) : 0;
-  }
-  __device__ int above(const RowsArgs& a, int per) const {   // sequences with more than t tiles
-    int c = 0;
-    for (int b = threadIdx.x & 31; b < a.B; b += 32) c += tiles(a, b, per) > t;
-    return __reduce_add_sync(0xffffffffu, c);
-  }
-  __device__ void begin(const RowsArgs& a, int per) {
-    int most = 0;
-    for (int b = threadIdx.x & 31; b < a.B; b += 32) most = max(most, tiles(a, b, per));
-    t = __reduce_max_sync(0xffffffffu, most) - 1;
-    count = t >= 0 ? above(a, per) : 0;
-  }
-  // Sequence of unit u's rows (and t: its tile number), or -1 past the last unit.
-  __device__ int find(const RowsArgs& a, int per, int u) {
-    while (t >= 0 && u >= before + count) {
-      before += count;
-      --t;
-      count = t >= 0 ? above(a, per) : 0;
-    }
-    if (t < 0) return -1;
-    int rank = u - before;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const unsigned votes = __ballot_sync(0xffffffffu, tiles(a, b0 + (threadIdx.x & 31), per) > t);
-      const int c = __popc(votes);
-      if (rank < c) return b0 + (int)__fns(votes, 0, rank + 1);
-      rank -= c;
-    }
-    return -1;
-  }
-};
 
 template <bool kPrefix>
 __device__ Unit decode(const RowsArgs& a, PromptWalk& walk, int u) {
@@ -156,7 +172,7 @@ __device__ Unit decode(const RowsArgs& a, PromptWalk& walk, int u) {
   w.tree = -1;
   w.part = 0;
   if (!kPrefix) {
-    const int b = walk.find(a, per, u / HG);
+    const int b = walk.find(u / HG);
     if (b < 0) return w;
     const int c0 = a.cu[b], len = a.cu[b + 1] - c0, i0 = walk.t * per;
     w.kind = kPrompt;
@@ -205,17 +221,19 @@ __device__ Unit decode(const RowsArgs& a, PromptWalk& walk, int u) {
   return w;
 }
 
-template <bool kPrefix>
+template <int kD, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKt,
                const __grid_constant__ CUtensorMap tmVt, const __grid_constant__ RowsArgs a) {
+  using Lay = Layout<kD>;
+  constexpr int kStages = Lay::stages, kTile = Lay::tile, kHalves = Lay::halves;
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* ring = sm + kOffRing;
+  uint8_t* ring = sm + Lay::ring;
   __shared__ __align__(8) uint64_t kv_full[kStages], kv_empty[kStages];
-  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2];
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_done[2];
   __shared__ __align__(8) uint64_t unit_full[2], unit_empty[2], tail;
   __shared__ Unit units[2];
   __shared__ uint32_t tmem_slot;
@@ -231,6 +249,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       tc::mbar_init(&q_full[t], 1);
       tc::mbar_init(&q_empty[t], 1);
       tc::mbar_init(&s_full[t], 1);
+      tc::mbar_init(&p_half[t], kRows);
       tc::mbar_init(&p_full[t], kRows);
       tc::mbar_init(&o_done[t], 1);
       tc::mbar_init(&unit_full[t], 1);
@@ -260,9 +279,11 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   if (warp == kPlanWarp) {
     // ------------------------------------------------------------------ schedule
     PromptWalk walk;
-    if (!kPrefix) walk.begin(a, 2 * npos);
+    if (!kPrefix) walk.begin(a.cu, a.B, a.T, 2 * npos);
     for (int i = 0;; ++i) {
-      const Unit w = decode<kPrefix>(a, walk, (int)blockIdx.x + i * (int)gridDim.x);
+      // units are ordered longest first; every other round is dealt in reverse, which evens out what the CTAs get
+      const int turn = (i & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
+      const Unit w = decode<kPrefix>(a, walk, turn + i * (int)gridDim.x);
       if (i >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&unit_empty[i & 1], ((i >> 1) - 1) & 1, err, 2))) break;
       if (lane == 0) {
         units[i & 1] = w;
@@ -288,8 +309,9 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           if (lane == 0) {
             uint8_t* dst = sm + s * kTile;
             tc::mbar_arrive_expect(&q_full[s], kTile);
-            tma_load_3d(dst, &tmQ, 0, w.pos0 + s * npos, w.h0, &q_full[s]);
-            tma_load_3d(dst + kHalf, &tmQ, 64, w.pos0 + s * npos, w.h0, &q_full[s]);
+#pragma unroll
+            for (int x = 0; x < kHalves; ++x)
+              tma_load_3d(dst + x * kHalf, &tmQ, 64 * x, w.pos0 + s * npos, w.h0, &q_full[s]);
           }
           ++nq[s];
         }
@@ -326,17 +348,17 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         uint64_t* bar = fix ? &tail : &kv_full[st];
         if (lane == 0) {
           tc::mbar_arrive_expect(bar, kTile);
-          tma_load_3d(dst, m, 0, y, z, bar);
-          tma_load_3d(dst + kHalf, m, 64, y, z, bar);
+#pragma unroll
+          for (int x = 0; x < kHalves; ++x) tma_load_3d(dst + x * kHalf, m, 64 * x, y, z, bar);
         }
         __syncwarp();
-        if (fix) {   // rows [live, 128) of both halves become zero before the MMA warp may see the tile
+        if (fix) {   // rows [live, 128) of each half become zero before the MMA warp may see the tile
           ok = __all_sync(0xffffffffu, tc::mbar_wait<true>(&tail, fixes & 1, err, 16));
           ++fixes;
           if (!ok) break;
           for (int c = live * 8 + lane; c < kKeys * 8; c += 32) {
-            reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
-            reinterpret_cast<uint4*>(dst + kHalf)[c] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < kHalves; ++x) reinterpret_cast<uint4*>(dst + x * kHalf)[c] = make_uint4(0, 0, 0, 0);
           }
           tc::fence_proxy_async();
           __syncwarp();
@@ -351,85 +373,99 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       if (nq[t] > 0) tc::mbar_wait(&q_full[t], (nq[t] - 1) & 1, err, 64);
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issue
-    // The whole warp walks the schedule; one elected lane issues.
+    // One elected lane walks the schedule and issues; little but waits stands between two
+    // batches of products, since whatever does is time without a product in flight (as a loop of
+    // the whole warp with a vote after each wait: 1520 us for a 16384-token prompt, so: 1370).
+    // What is left: a pair of tiles takes 2700 clocks for 2048 of products. Both operands of S
+    // come from shared memory, 8 KB per 64 clocks; with V and the arriving tiles the products
+    // ask for 2048 clocks of its bandwidth as well (TMEM has no room for Q beside S and O).
     constexpr uint32_t idS = tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
     constexpr uint32_t idPV = tc::idesc_bf16_f32(kRows, kD, 0, 1);
-    const uint64_t dQ = tc::sw128_desc(tc::saddr(sm), 16, 1024);
-    const uint64_t dK = tc::sw128_desc(tc::saddr(ring), 16, 1024);
-    const uint64_t dV = tc::sw128_desc(tc::saddr(ring), kHalf, 1024);   // MN-major: LBO = the 64-column half
-    Unit w;
-    int it = 0, nq[2] = {0, 0}, np[2] = {0, 0};   // ring position, Q tiles used, P tiles used
-    bool ok = true;
-    auto wait_kv = [&](int x) {
-      return __all_sync(0xffffffffu, tc::mbar_wait<true>(&kv_full[x % kStages], (x / kStages) & 1, err, 128));
-    };
-    // S_t = Q_t K^T with the K tile at ring position x; `last`: Q_t is not needed any more
-    auto issue_S = [&](int t, int x, bool last) {
-      tc::fence_after();
-      if (tc::elect_one()) {
-        const uint64_t q0 = dQ + (uint64_t)((t * kTile) >> 4), b0 = dK + (uint64_t)(((x % kStages) * kTile) >> 4);
+    if (tc::elect_one()) {
+      const uint64_t dQ = tc::sw128_desc(tc::saddr(sm), 16, 1024);
+      const uint64_t dK = tc::sw128_desc(tc::saddr(ring), 16, 1024);
+      const uint64_t dV = tc::sw128_desc(tc::saddr(ring), kHalf, 1024);   // MN-major: LBO = the 64-column half
+      int st = 0, ph = 0;                     // ring stage of the next tile and its phase
+      int nq[2] = {0, 0}, np[2] = {0, 0};     // Q tiles used, P tiles used
+      bool ok = true;
+      auto advance = [&](int& stage, int& phase) {
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      };
+      // S_t = Q_t K^T with the K tile in `stage`
+      auto issue_S = [&](int t, int stage) {
+        const uint64_t q0 = dQ + (uint64_t)((t * kTile) >> 4), b0 = dK + (uint64_t)((stage * kTile) >> 4);
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
           tc::mma_bf16(tmem + col_S(t), q0 + off, b0 + off, idS, kk > 0);
         }
         tc::commit(&s_full[t]);
-        if (last) tc::commit(&q_empty[t]);
-      }
-      __syncwarp();
-    };
-    // O_t (+)= P_t V with the V tile at ring position x
-    auto issue_PV = [&](int t, int x, bool first) {
-      tc::fence_after();
-      if (tc::elect_one()) {
-        const uint64_t b0 = dV + (uint64_t)(((x % kStages) * kTile) >> 4);
+      };
+      // O_t (+)= P_t V with keys [64 half, 64 half + 64) of the V tile in `stage`
+      auto issue_PV = [&](int t, int stage, int half, bool first) {
+        tc::fence_after();
+        const uint64_t b0 = dV + (uint64_t)((stage * kTile) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)   // keys [16 kk, 16 kk + 16): P columns 32 (kk / 2) + 8 (kk % 2)
+        for (int k4 = 0; k4 < kKeys / 32; ++k4) {   // keys [16 kk, 16 kk + 16): P columns 32 (kk / 2) + 8 (kk % 2)
+          const int kk = (kKeys / 32) * half + k4;
           tc::mma_bf16_tmem_a(tmem + col_O(t), tmem + col_S(t) + 32 * (kk >> 1) + 8 * (kk & 1),
-                              b0 + (uint64_t)((kk * 2048) >> 4), idPV, (!first || kk > 0) ? 1 : 0);
-        tc::commit(&o_done[t]);
-      }
-      __syncwarp();
-    };
-    auto release = [&](int x) {   // the stage is free once everything issued so far has read it
-      if (tc::elect_one()) tc::commit(&kv_empty[x % kStages]);
-      __syncwarp();
-    };
-    for (int i = 0; ok && next_unit(i, w); ++i) {
-      const int n[2] = {w.n0, w.n1}, nt = max(w.n0, w.n1);
-      if (nt == 0) continue;
-      ok = wait_kv(it);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (ok && n[t] > 0) {
-          ok = __all_sync(0xffffffffu, tc::mbar_wait<true>(&q_full[t], nq[t] & 1, err, 256));
-          ++nq[t];
-          if (ok) issue_S(t, it, n[t] == 1);
+                              b0 + (uint64_t)((kk * 2048) >> 4), idPV, (!first || k4 > 0) ? 1 : 0);
         }
-      }
-      if (!ok) break;
-      release(it);
-      for (int j = 0; ok && j < nt; ++j) {
-        const int xv = it + 2 * j + 1, xk = xv + 1;
-        ok = wait_kv(xv);
+      };
+      for (int i = 0; ok; ++i) {
+        ok = tc::mbar_wait(&unit_full[i & 1], (i >> 1) & 1, err, 1);
+        if (!ok) break;
+        const bool end = units[i & 1].kind == kEnd;
+        const int n[2] = {units[i & 1].n0, units[i & 1].n1}, nt = max(n[0], n[1]);
+        tc::mbar_arrive(&unit_empty[i & 1]);
+        if (end) break;
+        if (nt == 0) continue;
+        ok = mbar_poll(&kv_full[st], ph, err, 128);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (ok && j < n[t]) {
-            ok = __all_sync(0xffffffffu, tc::mbar_wait<true>(&p_full[t], np[t] & 1, err, 512));
-            ++np[t];
-            if (ok) issue_PV(t, xv, j == 0);
-            if (ok && j + 1 < n[t]) {
-              ok = wait_kv(xk);
-              if (ok) issue_S(t, xk, j + 2 == n[t]);
-            }
+          if (ok && n[t] > 0) {
+            ok = mbar_poll(&q_full[t], nq[t] & 1, err, 256);
+            ++nq[t];
+            if (ok) issue_S(t, st);
+            if (n[t] == 1) tc::commit(&q_empty[t]);
           }
         }
-        if (!ok) break;
-        release(xv);
-        if (j + 1 < nt) release(xk);
+        tc::commit(&kv_empty[st]);   // a stage is free once everything issued so far has read it
+        advance(st, ph);
+        for (int j = 0; ok && j < nt; ++j) {
+          const int sv = st, pv = ph;
+          advance(st, ph);
+          const int sk = st, pk = ph;
+          if (j + 1 < nt) advance(st, ph);
+          ok = mbar_poll(&kv_full[sv], pv, err, 128);
+          if (ok && j + 1 < nt) ok = mbar_poll(&kv_full[sk], pk, err, 128);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (ok && j < n[t]) {
+              ok = mbar_poll(&p_half[t], np[t] & 1, err, 4096);
+              if (!ok) break;
+              issue_PV(t, sv, 0, j == 0);
+              ok = mbar_poll(&p_full[t], np[t] & 1, err, 512);
+              if (!ok) break;
+              issue_PV(t, sv, 1, false);
+              ++np[t];
+              if (j + 1 < n[t]) {
+                issue_S(t, sk);
+                if (j + 2 == n[t]) tc::commit(&q_empty[t]);   // Q_t is not needed any more
+              } else {
+                tc::commit(&o_done[t]);
+              }
+            }
+          }
+          tc::commit(&kv_empty[sv]);
+          if (j + 1 < nt) tc::commit(&kv_empty[sk]);
+        }
       }
-      it += 2 * nt;
     }
+    __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax
     const int t = warp >> 2, row = 32 * (warp & 3) + lane;
@@ -437,7 +473,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const uint32_t tS = tmem + col_S(t) + lanes, tO = tmem + col_O(t) + lanes;
     const int rpos = t * npos + (row & (npos - 1)), rhead = row >> (7 - a.gp_shift);
     Unit w;
-    int ns = 0;   // S tiles taken
+    int ns = 0, nu = 0;   // S tiles and units taken
     bool ok = true;
     for (int i = 0; ok && next_unit(i, w); ++i) {
       const int n = t ? w.n1 : w.n0;
@@ -468,76 +504,80 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           uint32_t v[128];
 #pragma unroll
           for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + 32 * c, v + 32 * c);
-          tc::tmem_wait_ld();
-          if (kPrefix && j == w.tree) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (!(((c < 64 ? word0 : word1) >> (c & 63)) & 1ull)) v[c] = __float_as_uint(-INFINITY);
-          } else {
-            const int vis = limit - (w.k0 + j * kKeys);
-            if (__any_sync(0xffffffffu, vis < kKeys)) {
+          for (int c = 0; c < 4; ++c) tmem_landed32(v + 32 * c);
+          const int vis = limit - (w.k0 + j * kKeys);
+          const bool tree = kPrefix && j == w.tree, masked = tree || __any_sync(0xffffffffu, vis < kKeys);
+          auto mask64 = [&](uint32_t* x, int c0, uint64_t word) {   // scores of the keys [c0, c0 + 64) of the tile
 #pragma unroll
-              for (int c = 0; c < 128; ++c)
-                if (c >= vis) v[c] = __float_as_uint(-INFINITY);
-            }
+            for (int c = 0; c < 64; ++c)
+              if (tree ? !((word >> c) & 1ull) : c0 + c >= vis) x[c] = __float_as_uint(-INFINITY);
+          };
+          if (masked) {
+            mask64(v, 0, word0);
+            mask64(v + 64, 64, word1);
           }
-          float m4[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float m = __uint_as_float(v[32 * c]);
-#pragma unroll
-            for (int x = 1; x < 31; x += 2) m = max3(m, __uint_as_float(v[32 * c + x]), __uint_as_float(v[32 * c + x + 1]));
-            m4[c] = fmaxf(m, __uint_as_float(v[32 * c + 31]));
-          }
-          const float m_tile = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+          // The first 64 weights with the maximum as it stands, while the tile's own is found;
+          // again only where it has to move (and at the first tile).
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           float corr = 1.f;
-          if (m_tile > m_run + kLazy) {   // also on the first visible tile (m_run = -inf): corr = 0
-            corr = tc::ex2(m_run - m_tile);
-            m_run = m_tile;
-          }
-          const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
-          const float2 sc = make_float2(a.scale_log2, a.scale_log2), nm = make_float2(neg_m, neg_m);
-          float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+          uint32_t pk[16];
+          const bool fresh = __any_sync(0xffffffffu, m_run == -INFINITY);
+          if (!fresh) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const float2 e = __ffma2_rn(make_float2(__uint_as_float(v[32 * c + 2 * x]), __uint_as_float(v[32 * c + 2 * x + 1])),
-                                          sc, nm);
-              float2 p;
-              p.x = tc::ex2(e.x);
-              p.y = tc::ex2(e.y);
-              if (x & 1)
-                acc1 = __fadd2_rn(acc1, p);
-              else
-                acc0 = __fadd2_rn(acc0, p);
-              pk[x] = pack_bf16x2(p.x, p.y);
+            for (int c = 0; c < 2; ++c) {
+              exp32(v + 32 * c, a.scale_log2, -m_run, pk, acc);
+              tc::tmem_st16(tS + 32 * c, pk);   // P of keys [32 c, 32 c + 32) over the first half of their scores
             }
-            tc::tmem_st16(tS + 32 * c, pk);   // P of keys [32 c, 32 c + 32) over the first half of their scores
           }
-          const float2 s2 = __fadd2_rn(acc0, acc1);
-          l_run = l_run * corr + (s2.x + s2.y);
-          if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
-            // O += P_{j-1} V_{j-1} was issued before S_j and has landed with it
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tc::tmem_ld32(tO + 32 * c, o);
-              tc::tmem_wait_ld();
+          const float m_tile = fmaxf(fmaxf(max32(v), max32(v + 32)), fmaxf(max32(v + 64), max32(v + 96))) * a.scale_log2;
+          const bool move = m_tile > m_run + kLazy;   // also on the first visible tile (m_run = -inf): corr = 0
+          if (fresh || __any_sync(0xffffffffu, move)) {
+            if (move) {
+              corr = tc::ex2(m_run - m_tile);
+              m_run = m_tile;
+            }
+            const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+            acc[0] = acc[1] = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * corr);
-              tc::tmem_st32(tO + 32 * c, o);
+            for (int c = 0; c < 2; ++c) {
+              exp32(v + 32 * c, a.scale_log2, neg_m, pk, acc);
+              tc::tmem_st16(tS + 32 * c, pk);
+            }
+            if (j > 0) {   // O += P_{j-1} V_{j-1} was issued before S_j and has landed with it
+#pragma unroll 1
+              for (int c = 0; c < kD / 8; ++c) {
+                uint32_t o[8];
+                tc::tmem_ld8(tO + 8 * c, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * corr);
+                tc::tmem_st8(tO + 8 * c, o);
+              }
             }
           }
           tc::tmem_wait_st();
           tc::fence_before();
+          tc::mbar_arrive(&p_half[t]);   // the product with V begins on these 64 keys
+          const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+#pragma unroll
+          for (int c = 2; c < 4; ++c) {
+            exp32(v + 32 * c, a.scale_log2, neg_m, pk, acc);
+            tc::tmem_st16(tS + 32 * c, pk);
+          }
+          const float2 s2 = __fadd2_rn(acc[0], acc[1]);
+          l_run = l_run * corr + (s2.x + s2.y);
+          tc::tmem_wait_st();
+          tc::fence_before();
+        } else {
+          tc::mbar_arrive(&p_half[t]);
         }
         tc::mbar_arrive(&p_full[t]);
       }
       if (!ok) break;
       if (n > 0) {
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&o_done[t], (ns - 1) & 1, err, 2048));
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&o_done[t], nu & 1, err, 2048));
+        ++nu;
         if (!ok) break;
         tc::fence_after();
       }
@@ -546,7 +586,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       if (!kPrefix) {
         const float inv = l_run > 0.f ? 1.f / l_run : l_run;   // (a NaN sum stays NaN)
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kD / 32; ++c) {
           uint32_t o[32];
           tc::tmem_ld32(tO + 32 * c, o);
           tc::tmem_wait_ld();
@@ -566,7 +606,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const size_t prow = (size_t)w.part * a.T * a.Hq + orow;
         if (n > 0) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < kD / 32; ++c) {
             uint32_t o[32];
             tc::tmem_ld32(tO + 32 * c, o);
             tc::tmem_wait_ld();
@@ -594,6 +634,8 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   }
 }
 
+constexpr int kPrefixD = 128;
+
 // O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the splits; one warp per output row.
 __global__ void __launch_bounds__(256)
 rows_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml_part, int64_t rows, int splits,
@@ -611,7 +653,7 @@ rows_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml
     const float m = ml_part[2 * (s * rows + row)], ls = ml_part[2 * (s * rows + row) + 1];
     if (m == -INFINITY && ls == 0.f) continue;   // nothing was visible: its O need not have been written
     const float wgt = exp2f(m - M);
-    const float4 o = *reinterpret_cast<const float4*>(o_part + (s * rows + row) * kD + 4 * lane);
+    const float4 o = *reinterpret_cast<const float4*>(o_part + (s * rows + row) * kPrefixD + 4 * lane);
     l += wgt * ls;
     acc.x += wgt * o.x;
     acc.y += wgt * o.y;
@@ -619,15 +661,15 @@ rows_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml
     acc.w += wgt * o.w;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(O + row * kD + 4 * lane) =
+  *reinterpret_cast<uint2*>(O + row * kPrefixD + 4 * lane) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-// [planes][rows][128] bf16, boxes of 64 columns, `box_rows` rows and `box_planes` planes.
-bool encode_3d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t planes, uint64_t row_bytes, uint64_t plane_bytes,
+// [planes][rows][D] bf16, boxes of 64 columns, `box_rows` rows and `box_planes` planes.
+bool encode_3d(CUtensorMap* map, int D, const void* base, uint64_t rows, uint64_t planes, uint64_t row_bytes, uint64_t plane_bytes,
                uint32_t box_rows, uint32_t box_planes) {
   std::call_once(g_encode_once, [] {
     cudaDriverEntryPointQueryResult q;
@@ -637,7 +679,7 @@ bool encode_3d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t plane
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
   if (!g_encode) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)kD, rows, planes};
+  cuuint64_t dims[3] = {(cuuint64_t)D, rows, planes};
   cuuint64_t strides[2] = {row_bytes, plane_bytes};
   cuuint32_t box[3] = {64, box_rows, box_planes};
   cuuint32_t estr[3] = {1, 1, 1};
@@ -678,16 +720,16 @@ PrefixPlan plan_prefix(const medusa_cfg& c, int shared) {
   const int own = c.L_cap - ts.N - shared;
   split(uo, own > 0 ? own : 0, &p.splits_u, &p.chunk_u);
   const size_t rows = (size_t)c.B * ts.N * c.Hq, parts = p.splits_s + p.splits_u;
-  p.ml_part = align_up(parts * rows * kD * 4, 256);
+  p.ml_part = align_up(parts * rows * kPrefixD * 4, 256);
   p.total = p.ml_part + align_up(parts * rows * 8, 256);
   return p;
 }
 
-template <bool kPrefix>
+template <int D, bool kPrefix>
 cudaError_t launch_rows(const CUtensorMap* m, const RowsArgs& a, int64_t units, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<kPrefix>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<D, kPrefix>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(rows_tc_kernel<kPrefix>, (unsigned)(units < kSms ? units : kSms), kThreads, kSmem, st, m[0], m[1], m[2], m[3],
+  e = launch_pdl(rows_tc_kernel<D, kPrefix>, (unsigned)(units < kSms ? units : kSms), kThreads, Layout<D>::smem, st, m[0], m[1], m[2], m[3],
                  m[4], a);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -713,18 +755,18 @@ cudaError_t launch_prompt_tc(const medusa_cfg& c, const void* Q, const void* K, 
   a.Hq = c.Hq;
   a.Hkv = c.Hkv;
   a.gp_shift = gp_shift_of(c.Hq / c.Hkv);
-  a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)kD));
+  a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)c.D));
   a.O = static_cast<uint16_t*>(O);
   const int npos = kRows >> a.gp_shift;
   CUtensorMap m[5];
-  if (!encode_3d(&m[0], Q, T, c.Hq, q_stride * 2, kD * 2, npos, 1u << a.gp_shift) ||
-      !encode_3d(&m[1], K, T, c.Hkv, k_stride * 2, kD * 2, kKeys, 1) ||
-      !encode_3d(&m[2], V, T, c.Hkv, v_stride * 2, kD * 2, kKeys, 1))
+  if (!encode_3d(&m[0], c.D, Q, T, c.Hq, q_stride * 2, c.D * 2, npos, 1u << a.gp_shift) ||
+      !encode_3d(&m[1], c.D, K, T, c.Hkv, k_stride * 2, c.D * 2, kKeys, 1) ||
+      !encode_3d(&m[2], c.D, V, T, c.Hkv, v_stride * 2, c.D * 2, kKeys, 1))
     return cudaErrorInvalidValue;
   m[3] = m[1];
   m[4] = m[2];
   const int64_t units = ((int64_t)T / (2 * npos) + c.B) * (c.Hq >> a.gp_shift);   // at least as many as there are
-  return launch_rows<false>(m, a, units, st);
+  return c.D == 64 ? launch_rows<64, false>(m, a, units, st) : launch_rows<128, false>(m, a, units, st);
 }
 
 size_t prefix_workspace(const medusa_cfg& c, int shared) { return plan_prefix(c, shared).total; }
@@ -755,21 +797,21 @@ cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const vo
   a.chunk_s = p.chunk_s;
   a.splits_u = p.splits_u;
   a.chunk_u = p.chunk_u;
-  a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)kD));
+  a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)kPrefixD));
   a.o_part = static_cast<float*>(ws);
   a.ml_part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.ml_part);
   const int npos = kRows >> a.gp_shift, per = 2 * npos, HG = c.Hq >> a.gp_shift;
   const uint64_t planes = (uint64_t)num_pages * c.Hkv, tplanes = (uint64_t)c.B * c.Hkv;
   CUtensorMap m[5];
-  if (!encode_3d(&m[0], Q, a.T, c.Hq, (uint64_t)c.Hq * kD * 2, kD * 2, npos, 1u << a.gp_shift) ||
-      !encode_3d(&m[1], Kp, page_rows, planes, kD * 2, (uint64_t)page_rows * kD * 2, kKeys, 1) ||
-      !encode_3d(&m[2], Vp, page_rows, planes, kD * 2, (uint64_t)page_rows * kD * 2, kKeys, 1) ||
-      !encode_3d(&m[3], Kt, ts.N, tplanes, kD * 2, (uint64_t)ts.N * kD * 2, kKeys, 1) ||
-      !encode_3d(&m[4], Vt, ts.N, tplanes, kD * 2, (uint64_t)ts.N * kD * 2, kKeys, 1))
+  if (!encode_3d(&m[0], kPrefixD, Q, a.T, c.Hq, (uint64_t)c.Hq * kPrefixD * 2, kPrefixD * 2, npos, 1u << a.gp_shift) ||
+      !encode_3d(&m[1], kPrefixD, Kp, page_rows, planes, kPrefixD * 2, (uint64_t)page_rows * kPrefixD * 2, kKeys, 1) ||
+      !encode_3d(&m[2], kPrefixD, Vp, page_rows, planes, kPrefixD * 2, (uint64_t)page_rows * kPrefixD * 2, kKeys, 1) ||
+      !encode_3d(&m[3], kPrefixD, Kt, ts.N, tplanes, kPrefixD * 2, (uint64_t)ts.N * kPrefixD * 2, kKeys, 1) ||
+      !encode_3d(&m[4], kPrefixD, Vt, ts.N, tplanes, kPrefixD * 2, (uint64_t)ts.N * kPrefixD * 2, kKeys, 1))
     return cudaErrorInvalidValue;
   const int64_t units = (int64_t)p.splits_s * HG * ((a.T + per - 1) / per) +
                         (int64_t)p.splits_u * c.B * HG * ((ts.N + per - 1) / per);
-  cudaError_t e = launch_rows<true>(m, a, units, st);
+  cudaError_t e = launch_rows<kPrefixD, true>(m, a, units, st);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.T * c.Hq;
   e = launch_pdl(rows_merge_kernel, (unsigned)((rows * 32 + 255) / 256), 256, 0, st, static_cast<const float*>(a.o_part),
