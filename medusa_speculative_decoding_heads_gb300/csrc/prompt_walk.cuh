@@ -9,8 +9,8 @@ namespace medusa {
 
 // A sequence is cut into tiles of `per` rows; units are (tile number, sequence), by tile
 // number from the last one down, then by sequence, so that the longest units start first and
-// the shortest fill the end. A whole warp calls every function; units are asked for in
-// ascending order. Sequences whose bounds leave [0, T] or decrease have no tiles.
+// the shortest fill the end. A whole warp calls every function; units asked for in ascending
+// order cost little. Sequences whose bounds leave [0, T] or decrease have no tiles.
 struct PromptWalk {
   const int32_t* cu;
   int B, T, per;
@@ -39,6 +39,7 @@ struct PromptWalk {
   }
   // Sequence of unit u (t: its tile number), or -1 past the last unit.
   __device__ int find(int u) {
+    if (u < before) begin(cu, B, T, per);
     while (t >= 0 && u >= before + count) {
       before += count;
       --t;

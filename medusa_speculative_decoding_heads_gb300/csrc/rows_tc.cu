@@ -11,7 +11,7 @@
 // keys. A tile's rows are Gp query heads of the KV head's group times 128 / Gp positions
 // (Gp: the largest power of two that divides the group, at most 16), so that one TMA box
 // loads it and the heads share every K/V tile. 12 warps, one CTA per SM, which takes
-// units round by round:
+// units from the grid until none is left (warp 10):
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1: thread = row = TMEM lane; S (f32) to
 //                   registers, mask, maximum, 2^(s - m) rounded to bf16 back over S, sums
 //                   in f32. O is rescaled only when the maximum rises by more than 2^8.
@@ -23,7 +23,9 @@
 //   warp 9          TMA: Q tiles, then K and V tiles of 128 keys alternating through one
 //                   ring of 160 KB. V rows past the last key that may be read are zeroed in
 //                   shared memory (0 x NaN must not reach a result).
-//   warp 10         the schedule: decodes the next unit while the others work on this one.
+//   warp 10         the schedule: a unit per block of the grid, longest first; this warp takes over
+//                   blocks that have not started (cluster launch control) and decodes the next
+//                   unit while the others work on this one.
 // TMEM: S_0, S_1, O_0, O_1 (128 columns each; O uses D of them). Every mbarrier wait is bounded.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -57,6 +59,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSms = 152;
+constexpr int kAhead = 6;   // K and V tiles of a unit still to be loaded when the next unit is fetched
 // The running maximum moves (and O is rescaled) only when a tile's maximum exceeds it by more
 // than this many binary orders of magnitude: weights stay below 2^8, far inside bf16 and f32.
 constexpr float kLazy = 8.f;
@@ -104,6 +107,28 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+// Cluster launch control: asks for a block of this grid that has not started yet; its index
+// arrives as 16 bytes at `slot` (16-byte aligned), completing on `bar`.
+__device__ __forceinline__ void steal_ask(void* slot, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   tc::saddr(slot)),
+               "r"(tc::saddr(bar))
+               : "memory");
+}
+// The block index that was taken over, or -1: every block has started.
+__device__ __forceinline__ int steal_answer(const void* slot) {
+  uint32_t x, got;
+  asm volatile(
+      "{ .reg .pred p; .reg .b128 r; ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, _, _, _}, r; }"
+      : "=r"(x), "=r"(got)
+      : "r"(tc::saddr(slot))
+      : "memory");
+  return got ? (int)x : -1;
 }
 // mbarrier.test_wait: asks without being suspended.
 __device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
@@ -234,7 +259,8 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   uint8_t* ring = sm + Lay::ring;
   __shared__ __align__(8) uint64_t kv_full[kStages], kv_empty[kStages];
   __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_done[2];
-  __shared__ __align__(8) uint64_t unit_full[2], unit_empty[2], tail;
+  __shared__ __align__(8) uint64_t unit_full[2], unit_empty[2], tail, stolen, want;
+  __shared__ __align__(16) uint4 steal_slot[1];
   __shared__ Unit units[2];
   __shared__ uint32_t tmem_slot;
   uint32_t* err = &g_rows_tc_error;
@@ -256,6 +282,8 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       tc::mbar_init(&unit_empty[t], 10);   // 8 softmax warps, the MMA warp, the load warp
     }
     tc::mbar_init(&tail, 1);
+    tc::mbar_init(&stolen, 1);
+    tc::mbar_init(&want, 1);
     tc::mbar_fence_init();
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&tmem_slot, kTmemCols);
@@ -278,20 +306,45 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 
   if (warp == kPlanWarp) {
     // ------------------------------------------------------------------ schedule
+    // Block indices are units in order. The CTA begins with its own and then takes over blocks
+    // that have not started, so that the SMs run out of work together.
     PromptWalk walk;
     if (!kPrefix) walk.begin(a.cu, a.B, a.T, 2 * npos);
-    for (int i = 0;; ++i) {
-      // units are ordered longest first; every other round is dealt in reverse, which evens out what the CTAs get
-      const int turn = (i & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x;
-      const Unit w = decode<kPrefix>(a, walk, turn + i * (int)gridDim.x);
-      if (i >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&unit_empty[i & 1], ((i >> 1) - 1) & 1, err, 2))) break;
+    int u = (int)blockIdx.x, asked = 0, i = 0;   // i: units handed out
+    bool ok = true;
+    while (ok && u >= 0) {
+      const Unit w = decode<kPrefix>(a, walk, u);
+      if (w.kind != kEnd) {   // (the grid may hold more blocks than there are units)
+        if (i >= 2) ok = __all_sync(0xffffffffu, tc::mbar_wait(&unit_empty[i & 1], ((i >> 1) - 1) & 1, err, 2));
+        if (!ok) break;
+        if (lane == 0) {
+          units[i & 1] = w;
+          tc::mbar_arrive(&unit_full[i & 1]);
+        }
+        __syncwarp();
+        // not before the loads of this unit near their end: what is taken too early is missing elsewhere
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&want, i & 1, err, 16384));
+        ++i;
+        if (!ok) break;
+      }
       if (lane == 0) {
-        units[i & 1] = w;
-        tc::mbar_arrive(&unit_full[i & 1]);
+        tc::mbar_arrive_expect(&stolen, 16);
+        steal_ask(steal_slot, &stolen);
       }
       __syncwarp();
-      if (w.kind == kEnd) break;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&stolen, asked & 1, err, 8192));
+      ++asked;
+      if (!ok) break;
+      u = steal_answer(steal_slot);
+      tc::fence_proxy_async();   // the slot has been read before the next answer may land in it
+      __syncwarp();
     }
+    if (i >= 2) tc::mbar_wait(&unit_empty[i & 1], ((i >> 1) - 1) & 1, err, 2);
+    if (lane == 0) {
+      units[i & 1].kind = kEnd;
+      tc::mbar_arrive(&unit_full[i & 1]);
+    }
+    __syncwarp();
   } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ TMA loads
     Unit w;
@@ -300,7 +353,9 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     for (int i = 0; ok && next_unit(i, w); ++i) {
       const int nt = max(w.n0, w.n1);
       int page_reg = 0;
+      if (nt == 0 && lane == 0) tc::mbar_arrive(&want);
       for (int s = 0; ok && s < 2 * nt; ++s) {   // K_0, V_0, K_1, V_1, ...
+        if (s == max(2 * nt - kAhead, 0) && lane == 0) tc::mbar_arrive(&want);   // time to fetch the next unit
         const int j = s >> 1;
         const bool isv = s & 1;
         if (s < 2 && (s == 0 ? w.n0 : w.n1) > 0) {   // Q tile s, ahead of its first use
@@ -729,7 +784,7 @@ template <int D, bool kPrefix>
 cudaError_t launch_rows(const CUtensorMap* m, const RowsArgs& a, int64_t units, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<D, kPrefix>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(rows_tc_kernel<D, kPrefix>, (unsigned)(units < kSms ? units : kSms), kThreads, Layout<D>::smem, st, m[0], m[1], m[2], m[3],
+  e = launch_pdl(rows_tc_kernel<D, kPrefix>, (unsigned)units, kThreads, Layout<D>::smem, st, m[0], m[1], m[2], m[3],
                  m[4], a);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
