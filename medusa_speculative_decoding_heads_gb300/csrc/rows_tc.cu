@@ -180,6 +180,26 @@ __device__ __forceinline__ void exp32(const uint32_t* v, float scale_log2, float
     pk[x] = pack_bf16x2(p.x, p.y);
   }
 }
+// Four lanes hold four 16-byte pieces of a row each (r[4 i ..]: piece i); afterwards lane l of
+// the four holds piece l of rows 0..3 (r[4 k ..]: row k).
+__device__ __forceinline__ void transpose4(uint32_t* r) {
+  const int lane = threadIdx.x;
+#pragma unroll
+  for (int s = 1; s <= 2; s <<= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & s) continue;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t &lo = r[4 * i + x], &hi = r[4 * (i | s) + x];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
+        if (up) lo = got;
+        else hi = got;
+      }
+    }
+  }
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -442,7 +462,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       const uint64_t dV = tc::sw128_desc(tc::saddr(ring), kHalf, 1024);   // MN-major: LBO = the 64-column half
       int st = 0, ph = 0;                     // ring stage of the next tile and its phase
       int nq[2] = {0, 0}, np[2] = {0, 0};     // Q tiles used, P tiles used
-      bool ok = true;
+      bool ok = true, ahead = false;          // ahead: S_0(0) of the coming unit has been issued
       auto advance = [&](int& stage, int& phase) {
         if (++stage == kStages) {
           stage = 0;
@@ -481,13 +501,14 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         ok = mbar_poll(&kv_full[st], ph, err, 128);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (ok && n[t] > 0) {
+          if (ok && n[t] > 0 && !(t == 0 && ahead)) {
             ok = mbar_poll(&q_full[t], nq[t] & 1, err, 256);
             ++nq[t];
             if (ok) issue_S(t, st);
             if (n[t] == 1) tc::commit(&q_empty[t]);
           }
         }
+        ahead = false;
         tc::commit(&kv_empty[st]);   // a stage is free once everything issued so far has read it
         advance(st, ph);
         for (int j = 0; ok && j < nt; ++j) {
@@ -512,6 +533,18 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 if (j + 2 == n[t]) tc::commit(&q_empty[t]);   // Q_t is not needed any more
               } else {
                 tc::commit(&o_done[t]);
+              }
+            }
+            // Tile 0 is through with the unit: its first product of the next one goes ahead of tile
+            // 1's last, if everything for it is there.
+            if (ok && t == 0 && j + 1 == nt && mbar_test(&unit_full[(i + 1) & 1], ((i + 1) >> 1) & 1)) {
+              const int n0 = units[(i + 1) & 1].n0;
+              if (units[(i + 1) & 1].kind != kEnd && n0 > 0 && mbar_test(&kv_full[st], ph) && mbar_test(&q_full[0], nq[0] & 1)) {
+                tc::fence_after();
+                ++nq[0];
+                issue_S(0, st);
+                if (n0 == 1) tc::commit(&q_empty[0]);
+                ahead = true;
               }
             }
           }
@@ -637,44 +670,51 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tc::fence_after();
       }
       if (!busy) continue;
-      const size_t orow = (size_t)pos * a.Hq + head;
+      // Four lanes hold four consecutive positions of one head. They trade 16-byte pieces, so that
+      // a store instruction writes 64 bytes of each row, not 16 (a quarter of the memory lines).
+      const int quad = lane & 3;
+      const size_t orow = (size_t)pos * a.Hq + head, orow0 = (size_t)(pos - quad) * a.Hq + head;
+      const int rows_here = w.left - (rpos - quad);   // rows of the four that exist, if positive
       if (!kPrefix) {
         const float inv = l_run > 0.f ? 1.f / l_run : l_run;   // (a NaN sum stays NaN)
 #pragma unroll 1
         for (int c = 0; c < kD / 32; ++c) {
-          uint32_t o[32];
+          uint32_t o[32], pk[16];
           tc::tmem_ld32(tO + 32 * c, o);
-          tc::tmem_wait_ld();
-          if (row_ok) {
-            uint4* op = reinterpret_cast<uint4*>(a.O + orow * kD + 32 * c);
+          tmem_landed32(o);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t pk[4];
+          for (int x = 0; x < 16; ++x)
+            pk[x] = pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
+          transpose4(pk);
+          uint16_t* op = a.O + orow0 * kD + 32 * c + 8 * quad;
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                pk[y] = pack_bf16x2(__uint_as_float(o[8 * x + 2 * y]) * inv, __uint_as_float(o[8 * x + 2 * y + 1]) * inv);
-              op[x] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            }
-          }
+          for (int k = 0; k < 4; ++k)
+            if (k < rows_here)
+              *reinterpret_cast<uint4*>(op + (size_t)k * a.Hq * kD) = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
         }
       } else {
-        const size_t prow = (size_t)w.part * a.T * a.Hq + orow;
+        const size_t part = (size_t)w.part * a.T * a.Hq;
         if (n > 0) {
 #pragma unroll 1
           for (int c = 0; c < kD / 32; ++c) {
             uint32_t o[32];
             tc::tmem_ld32(tO + 32 * c, o);
-            tc::tmem_wait_ld();
-            if (row_ok) {
-              uint4* op = reinterpret_cast<uint4*>(a.o_part + prow * kD + 32 * c);
+            tmem_landed32(o);
 #pragma unroll
-              for (int x = 0; x < 8; ++x) op[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            for (int x = 0; x < 2; ++x) {
+              transpose4(o + 16 * x);
+              float* op = a.o_part + (part + orow0) * kD + 32 * c + 16 * x + 4 * quad;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k < rows_here)
+                  *reinterpret_cast<uint4*>(op + (size_t)k * a.Hq * kD) =
+                      make_uint4(o[16 * x + 4 * k], o[16 * x + 4 * k + 1], o[16 * x + 4 * k + 2], o[16 * x + 4 * k + 3]);
             }
           }
         }
         if (row_ok) {
-          a.ml_part[2 * prow] = m_run;
-          a.ml_part[2 * prow + 1] = l_run;
+          a.ml_part[2 * (part + orow)] = m_run;
+          a.ml_part[2 * (part + orow) + 1] = l_run;
         }
       }
       tc::fence_before();   // O has been read before the next unit's first P is announced
