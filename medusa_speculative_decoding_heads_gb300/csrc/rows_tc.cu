@@ -34,6 +34,7 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "prompt_walk.cuh"
@@ -59,7 +60,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSms = 152;
-constexpr int kAhead = 6;   // K and V tiles of a unit still to be loaded when the next unit is fetched
+constexpr int kAhead = 6;   // steps (K and V tiles) of a unit still to be loaded when the next unit is fetched
 // The running maximum moves (and O is rescaled) only when a tile's maximum exceeds it by more
 // than this many binary orders of magnitude: weights stay below 2^8, far inside bf16 and f32.
 constexpr float kLazy = 8.f;
@@ -76,7 +77,8 @@ struct RowsArgs {
   int B, N, T;             // T: rows of Q (prefix: B * N)
   int Hq, Hkv, gp_shift;   // log2 of Gp
   int L_cap, page_rows, max_pages, num_pages, shared;
-  int splits_s, chunk_s, splits_u, chunk_u;   // key splits of the shared and of the own rows
+  int units_s, splits_s, chunk_s, dual_s;   // units, key ranges and their length of the shared rows; 1: dual units
+  int units_u, splits_u, chunk_u, dual_u;   // the same of the sequences' own rows
   float scale_log2;
   uint16_t* O;             // prompts
   float* o_part;           // prefix: [split][row][D], row = position * Hq + head
@@ -85,17 +87,17 @@ struct RowsArgs {
 
 enum UnitKind : int { kEnd = 0, kPrompt = 1, kShared = 2, kOwn = 3 };
 
-// What the scheduling warp hands to the others.
+// What the scheduling warp hands to the others. Where the rows of a key range fill one tile only
+// (prefix), the two tiles are two such pieces of work, so that there is still one tile's softmax
+// to hide behind the other's products; they then share no K/V tile (`dual`).
 struct Unit {
-  int kind;
-  int pos0;      // Q row (position) of tile 0's first row; tile 1 begins 128 / Gp later
-  int left;      // positions from pos0 on that exist
-  int h0, kvh;   // first query head, KV head
-  int n0, n1;    // key tiles of tile 0 and tile 1 (the tree tile included)
-  int k0, kend;  // key range
-  int base;      // prompts: packed row of the sequence's row 0; prefix: the sequence
-  int tree;      // number of the tree tile, or -1
-  int part;      // prefix: split the partial result belongs to
+  int kind, dual;
+  int pos0[2], left[2];   // a tile's first Q row (position), and how many positions there are from it on
+  int h0[2], kvh[2];      // first query head, KV head
+  int base[2];            // prompts: packed row of the sequence's row 0; prefix: the sequence
+  int k0[2], kend[2];     // key range
+  int n[2], tree[2];      // key tiles (the tree tile included); number of the tree tile, or -1
+  int part[2];            // prefix: which partial result the tile writes
 };
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -208,61 +210,69 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-template <bool kPrefix>
-__device__ Unit decode(const RowsArgs& a, PromptWalk& walk, int u) {
-  Unit w;
-  const int npos = kRows >> a.gp_shift, per = 2 * npos;   // positions of a tile, of a unit
-  const int G = a.Hq / a.Hkv, HG = a.Hq >> a.gp_shift;
-  w.kind = kEnd;
+// One tile's part of a unit, as decoded by lanes t, t + 2, ... of the scheduling warp. (What runs
+// once per unit is kept short: between two units its instructions come from beyond the
+// instruction caches, which the softmax fills.)
+struct Piece {
+  int kind, dual, pos0, left, h0, kvh, base, k0, kend, n, tree, part;
+};
+
+// Unit u of the prompts: 256 rows, both tiles over the same keys.
+__device__ __forceinline__ Piece decode_prompt(const RowsArgs& a, PromptWalk& walk, int u, int t) {
+  Piece w = {};
+  const int npos = kRows >> a.gp_shift, HG = a.Hq >> a.gp_shift;
+  const int b = walk.find(u / HG);
+  if (b < 0) return w;
+  const int c0 = a.cu[b], len = a.cu[b + 1] - c0, i = (2 * walk.t + t) * npos;
+  w.kind = kPrompt;
+  w.pos0 = c0 + i;
+  w.left = len - i;
+  w.h0 = (u % HG) << a.gp_shift;
+  w.kvh = w.h0 / (a.Hq / a.Hkv);
+  w.base = c0;
+  w.kend = len;
+  w.n = i < len ? (min(len, i + npos) + kKeys - 1) / kKeys : 0;
   w.tree = -1;
-  w.part = 0;
-  if (!kPrefix) {
-    const int b = walk.find(u / HG);
-    if (b < 0) return w;
-    const int c0 = a.cu[b], len = a.cu[b + 1] - c0, i0 = walk.t * per;
-    w.kind = kPrompt;
-    w.pos0 = c0 + i0;
-    w.left = len - i0;
-    w.h0 = (u % HG) << a.gp_shift;
-    w.k0 = 0;
-    w.kend = len;
-    w.base = c0;
-    w.n0 = (min(len, i0 + npos) + kKeys - 1) / kKeys;
-    w.n1 = w.left > npos ? (min(len, i0 + per) + kKeys - 1) / kKeys : 0;
+  return w;
+}
+
+// Unit u of tree attention behind a prefix: the shared rows come first, for all positions of the
+// batch (a.units_s units), then the sequences' own rows and trees (a.units_u).
+__device__ __forceinline__ Piece decode_prefix(const RowsArgs& a, int u, int t) {
+  Piece w = {};
+  const int npos = kRows >> a.gp_shift, HG = a.Hq >> a.gp_shift;
+  if (u >= a.units_s + a.units_u) return w;
+  const bool shared = u < a.units_s;
+  w.kind = shared ? kShared : kOwn;
+  w.dual = shared ? a.dual_s : a.dual_u;
+  w.tree = -1;
+  const int v = shared ? u : u - a.units_s;
+  const int positions = shared ? a.T : a.N;   // that meet the same keys
+  // piece x: (split, [sequence,] head group), for the two tiles together or for one
+  const int per = w.dual ? npos : 2 * npos, ru = (positions + per - 1) / per;
+  const int vt = w.dual ? 2 * v + t : v, x = vt / ru, row0 = (vt - x * ru) * per + (w.dual ? 0 : t * npos);
+  const int y = x / HG, split = shared ? y : y / a.B, b = shared ? 0 : y - split * a.B;
+  w.left = positions - row0;
+  if (split >= (shared ? a.splits_s : a.splits_u)) w.left = 0;   // the last unit of an odd number of pieces
+  if (w.left <= 0) return w;
+  w.pos0 = b * a.N + row0;
+  w.h0 = (x - y * HG) << a.gp_shift;
+  w.kvh = w.h0 / (a.Hq / a.Hkv);
+  w.base = b;
+  w.part = shared ? split : a.splits_s + split;
+  bool tree = false;
+  if (shared) {
+    w.k0 = split * a.chunk_s;
+    w.kend = min(a.shared, w.k0 + a.chunk_s);
   } else {
-    const int rows = a.T, ru = (rows + per - 1) / per, us = a.splits_s * HG * ru;
-    const int nu = (a.N + per - 1) / per;
-    if (u < us) {   // shared rows: all positions of the batch
-      const int r = u / ru, split = r / HG;
-      w.kind = kShared;
-      w.pos0 = (u % ru) * per;
-      w.left = rows - w.pos0;
-      w.h0 = (r % HG) << a.gp_shift;
-      w.k0 = split * a.chunk_s;
-      w.kend = min(a.shared, w.k0 + a.chunk_s);
-      w.base = 0;
-      w.part = split;
-      w.n0 = (w.kend - w.k0) / kKeys;
-    } else {        // a sequence's own rows and tree
-      const int v = u - us, r = v / nu, hb = r / HG, b = hb % a.B, split = hb / a.B;
-      if (split >= a.splits_u) return w;
-      const int Lb = a.L[b];
-      const bool ok = Lb >= 0 && Lb <= a.L_cap - a.N;
-      const int node0 = (v % nu) * per;
-      w.kind = kOwn;
-      w.pos0 = b * a.N + node0;
-      w.left = a.N - node0;
-      w.h0 = (r % HG) << a.gp_shift;
-      w.k0 = a.shared + split * a.chunk_u;
-      w.kend = ok ? min(Lb, w.k0 + a.chunk_u) : 0;
-      w.base = b;
-      w.part = a.splits_s + split;
-      w.n0 = w.kend > w.k0 ? (w.kend - w.k0 + kKeys - 1) / kKeys : 0;
-      if (ok && split == a.splits_u - 1) w.tree = w.n0++;
-    }
-    w.n1 = w.left > npos ? w.n0 : 0;
+    const int Lb = a.L[b];
+    const bool ok = Lb >= 0 && Lb <= a.L_cap - a.N;
+    w.k0 = a.shared + split * a.chunk_u;
+    w.kend = ok ? min(Lb, w.k0 + a.chunk_u) : 0;
+    tree = ok && split == a.splits_u - 1;
   }
-  w.kvh = w.h0 / G;
+  w.n = w.kend > w.k0 ? (w.kend - w.k0 + kKeys - 1) / kKeys : 0;
+  if (tree) w.tree = w.n++;
   return w;
 }
 
@@ -333,14 +343,28 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     int u = (int)blockIdx.x, asked = 0, i = 0;   // i: units handed out
     bool ok = true;
     while (ok && u >= 0) {
-      const Unit w = decode<kPrefix>(a, walk, u);
+      const int t = lane & 1;
+      const Piece w = kPrefix ? decode_prefix(a, u, t) : decode_prompt(a, walk, u, t);
       if (w.kind != kEnd) {   // (the grid may hold more blocks than there are units)
         if (i >= 2) ok = __all_sync(0xffffffffu, tc::mbar_wait(&unit_empty[i & 1], ((i >> 1) - 1) & 1, err, 2));
         if (!ok) break;
-        if (lane == 0) {
-          units[i & 1] = w;
-          tc::mbar_arrive(&unit_full[i & 1]);
+        Unit& d = units[i & 1];
+        if (lane < 2) {
+          d.kind = w.kind;
+          d.dual = w.dual;
+          d.pos0[t] = w.pos0;
+          d.left[t] = w.left;
+          d.h0[t] = w.h0;
+          d.kvh[t] = w.kvh;
+          d.base[t] = w.base;
+          d.k0[t] = w.k0;
+          d.kend[t] = w.kend;
+          d.n[t] = w.n;
+          d.tree[t] = w.tree;
+          d.part[t] = w.part;
         }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&unit_full[i & 1]);
         __syncwarp();
         // not before the loads of this unit near their end: what is taken too early is missing elsewhere
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&want, i & 1, err, 16384));
@@ -367,79 +391,95 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     __syncwarp();
   } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ TMA loads
+    // Tiles come in the order in which the MMA warp uses them: K_0, V_0, K_1, V_1, ...; for two
+    // tiles with keys of their own K_0 K'_0, V_0 K_1 V'_0 K'_1, ...
     Unit w;
     int it = 0, nq[2] = {0, 0}, fixes = 0;   // ring position, Q tiles loaded, tails zeroed
+    int page_reg[2] = {-1, -1};
     bool ok = true;
     for (int i = 0; ok && next_unit(i, w); ++i) {
-      const int nt = max(w.n0, w.n1);
-      int page_reg = 0;
-      if (nt == 0 && lane == 0) tc::mbar_arrive(&want);
-      for (int s = 0; ok && s < 2 * nt; ++s) {   // K_0, V_0, K_1, V_1, ...
-        if (s == max(2 * nt - kAhead, 0) && lane == 0) tc::mbar_arrive(&want);   // time to fetch the next unit
-        const int j = s >> 1;
-        const bool isv = s & 1;
-        if (s < 2 && (s == 0 ? w.n0 : w.n1) > 0) {   // Q tile s, ahead of its first use
-          if (nq[s] > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty[s], (nq[s] - 1) & 1, err, 4));
+      const int nt = max(w.n[0], w.n[1]), tiles = w.dual ? 2 : 1;
+      if (nt <= kAhead && lane == 0) tc::mbar_arrive(&want);   // time to fetch the next unit
+#pragma unroll 1
+      for (int j = nt > 0 ? -1 : 0; ok && j < nt; ++j) {   // step j: V_j and K_{j+1}
+        if (j > 0 && nt - j == kAhead && lane == 0) tc::mbar_arrive(&want);
+#pragma unroll 1
+        for (int x = 0; ok && x < 2 * tiles; ++x) {
+          const int t = x >> 1, n = w.dual ? (t ? w.n[1] : w.n[0]) : nt, jt = j + (x & 1);
+          const bool isv = !(x & 1);
+          if (jt < 0 || jt >= n) continue;
+          // a tile's rows go ahead of its first K tile; tile 1's, where both share the keys, behind it
+          const int r = j < 0 ? t : (j == 0 && x == 0 && !w.dual && w.n[1] > 0) ? 1 : -1;
+          if (r >= 0) {
+            const int used = r ? nq[1] : nq[0];
+            if (used > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty[r], (used - 1) & 1, err, 4));
+            if (!ok) break;
+            if (lane == 0) {
+              uint8_t* dst = sm + r * kTile;
+              tc::mbar_arrive_expect(&q_full[r], kTile);
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h)
+                tma_load_3d(dst + h * kHalf, &tmQ, 64 * h, r ? w.pos0[1] : w.pos0[0], r ? w.h0[1] : w.h0[0], &q_full[r]);
+            }
+            if (r) ++nq[1];
+            else ++nq[0];
+          }
+          const int k0 = t ? w.k0[1] : w.k0[0], kend = t ? w.kend[1] : w.kend[0], base = t ? w.base[1] : w.base[0];
+          const int kvh = t ? w.kvh[1] : w.kvh[0];
+          const int st = it % kStages;
+          if (it >= kStages) ok = __all_sync(0xffffffffu, tc::mbar_wait<true>(&kv_empty[st], (it / kStages - 1) & 1, err, 8));
           if (!ok) break;
+          const bool tree = kPrefix && jt == (t ? w.tree[1] : w.tree[0]);
+          const int key0 = k0 + jt * kKeys;
+          int y, z;
+          if (!kPrefix) {
+            y = base + key0;
+            z = kvh;
+          } else if (tree) {
+            y = 0;
+            z = base * a.Hkv + kvh;
+          } else {
+            int pages = t ? page_reg[1] : page_reg[0];
+            if (!isv && (jt & 31) == 0) {   // 32 tiles' pages at a time, one per lane
+              const int key = key0 + lane * kKeys;
+              pages = -1;
+              if (key < kend)
+                pages = w.kind == kShared ? a.prefix[key / a.page_rows] : a.table[(size_t)base * a.max_pages + key / a.page_rows];
+              if (t) page_reg[1] = pages;
+              else page_reg[0] = pages;
+            }
+            const int page = __shfl_sync(0xffffffffu, pages, jt & 31);
+            const bool in_pool = page >= 0 && page < a.num_pages;
+            MEDUSA_CHECK(isv || lane != 0 || in_pool, MEDUSA_CHECK_PAGE);
+            y = key0 % a.page_rows;
+            z = (in_pool ? page : a.num_pages) * a.Hkv + kvh;   // outside the pool: TMA fills zeros
+          }
+          const CUtensorMap* m = tree ? (isv ? &tmVt : &tmKt) : (isv ? &tmV : &tmK);
+          uint8_t* dst = ring + st * kTile;
+          const int live = tree ? kKeys : min(kKeys, kend - key0);   // (rows past the tree's nodes arrive as zeros)
+          const bool fix = isv && live < kKeys;
+          uint64_t* bar = fix ? &tail : &kv_full[st];
           if (lane == 0) {
-            uint8_t* dst = sm + s * kTile;
-            tc::mbar_arrive_expect(&q_full[s], kTile);
+            tc::mbar_arrive_expect(bar, kTile);
 #pragma unroll
-            for (int x = 0; x < kHalves; ++x)
-              tma_load_3d(dst + x * kHalf, &tmQ, 64 * x, w.pos0 + s * npos, w.h0, &q_full[s]);
+            for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * kHalf, m, 64 * h, y, z, bar);
           }
-          ++nq[s];
-        }
-        const int st = it % kStages;
-        if (it >= kStages) ok = __all_sync(0xffffffffu, tc::mbar_wait<true>(&kv_empty[st], (it / kStages - 1) & 1, err, 8));
-        if (!ok) break;
-        const bool tree = kPrefix && j == w.tree;
-        const int key0 = w.k0 + j * kKeys;
-        int y, z;
-        if (!kPrefix) {
-          y = w.base + key0;
-          z = w.kvh;
-        } else if (tree) {
-          y = 0;
-          z = w.base * a.Hkv + w.kvh;
-        } else {
-          if (!isv && (j & 31) == 0) {   // 32 tiles' pages at a time, one per lane
-            const int key = w.k0 + (j + lane) * kKeys;
-            page_reg = -1;
-            if (key < w.kend)
-              page_reg = w.kind == kShared ? a.prefix[key / a.page_rows]
-                                           : a.table[(size_t)w.base * a.max_pages + key / a.page_rows];
-          }
-          const int page = __shfl_sync(0xffffffffu, page_reg, j & 31);
-          const bool in_pool = page >= 0 && page < a.num_pages;
-          MEDUSA_CHECK(isv || lane != 0 || in_pool, MEDUSA_CHECK_PAGE);
-          y = key0 % a.page_rows;
-          z = (in_pool ? page : a.num_pages) * a.Hkv + w.kvh;   // outside the pool: TMA fills zeros
-        }
-        const CUtensorMap* m = tree ? (isv ? &tmVt : &tmKt) : (isv ? &tmV : &tmK);
-        uint8_t* dst = ring + st * kTile;
-        const int live = tree ? kKeys : min(kKeys, w.kend - key0);   // (rows past the tree's nodes arrive as zeros)
-        const bool fix = isv && live < kKeys;
-        uint64_t* bar = fix ? &tail : &kv_full[st];
-        if (lane == 0) {
-          tc::mbar_arrive_expect(bar, kTile);
-#pragma unroll
-          for (int x = 0; x < kHalves; ++x) tma_load_3d(dst + x * kHalf, m, 64 * x, y, z, bar);
-        }
-        __syncwarp();
-        if (fix) {   // rows [live, 128) of each half become zero before the MMA warp may see the tile
-          ok = __all_sync(0xffffffffu, tc::mbar_wait<true>(&tail, fixes & 1, err, 16));
-          ++fixes;
-          if (!ok) break;
-          for (int c = live * 8 + lane; c < kKeys * 8; c += 32) {
-#pragma unroll
-            for (int x = 0; x < kHalves; ++x) reinterpret_cast<uint4*>(dst + x * kHalf)[c] = make_uint4(0, 0, 0, 0);
-          }
-          tc::fence_proxy_async();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&kv_full[st]);
+          if (fix) {   // rows [live, 128) of each half become zero before the MMA warp may see the tile
+            ok = __all_sync(0xffffffffu, tc::mbar_wait<true>(&tail, fixes & 1, err, 16));
+            ++fixes;
+            if (!ok) break;
+#pragma unroll 1
+            for (int c = live * 8 + lane; c < kKeys * 8; c += 32) {
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h) reinterpret_cast<uint4*>(dst + h * kHalf)[c] = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&kv_full[st]);
+          }
+          ++it;
         }
-        ++it;
       }
     }
     // never leave with copies still landing in shared memory
@@ -490,38 +530,47 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                               b0 + (uint64_t)((kk * 2048) >> 4), idPV, (!first || k4 > 0) ? 1 : 0);
         }
       };
-      for (int i = 0; ok; ++i) {
-        ok = tc::mbar_wait(&unit_full[i & 1], (i >> 1) & 1, err, 1);
-        if (!ok) break;
-        const bool end = units[i & 1].kind == kEnd;
-        const int n[2] = {units[i & 1].n0, units[i & 1].n1}, nt = max(n[0], n[1]);
-        tc::mbar_arrive(&unit_empty[i & 1]);
-        if (end) break;
-        if (nt == 0) continue;
-        ok = mbar_poll(&kv_full[st], ph, err, 128);
+      // One unit, number i of this CTA. (A template of `dual`: a test between two batches of products
+      // shows, 228 -> 270 us for 32 trees behind 8192 rows.)
+      auto issue_unit = [&](auto dual_c, int i, const int* n) {
+        constexpr bool dual = decltype(dual_c)::value;
+        const int nt = max(n[0], n[1]);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (ok && n[t] > 0 && !(t == 0 && ahead)) {
-            ok = mbar_poll(&q_full[t], nq[t] & 1, err, 256);
+          if (!ok || n[t] == 0) continue;
+          if (!(t == 0 && ahead)) {
+            ok = mbar_poll(&kv_full[st], ph, err, 128) && mbar_poll(&q_full[t], nq[t] & 1, err, 256);
+            if (!ok) break;
             ++nq[t];
-            if (ok) issue_S(t, st);
+            issue_S(t, st);
             if (n[t] == 1) tc::commit(&q_empty[t]);
+          }
+          if (dual) {   // a stage is free once everything issued so far has read it
+            tc::commit(&kv_empty[st]);
+            advance(st, ph);
           }
         }
         ahead = false;
-        tc::commit(&kv_empty[st]);   // a stage is free once everything issued so far has read it
-        advance(st, ph);
-        for (int j = 0; ok && j < nt; ++j) {
-          const int sv = st, pv = ph;
+        if (!dual) {
+          tc::commit(&kv_empty[st]);
           advance(st, ph);
-          const int sk = st, pk = ph;
-          if (j + 1 < nt) advance(st, ph);
-          ok = mbar_poll(&kv_full[sv], pv, err, 128);
-          if (ok && j + 1 < nt) ok = mbar_poll(&kv_full[sk], pk, err, 128);
+        }
+        for (int j = 0; ok && j < nt; ++j) {
+          int sv = 0, sk = 0;   // stages of V_j and K_{j+1}
+          auto take = [&](int& stage) {
+            stage = st;
+            ok = ok && mbar_poll(&kv_full[st], ph, err, 128);
+            advance(st, ph);
+          };
+          if (!dual) {
+            take(sv);
+            if (j + 1 < nt) take(sk);
+          }
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (ok && j < n[t]) {
-              ok = mbar_poll(&p_half[t], np[t] & 1, err, 4096);
+              if (dual) take(sv);
+              ok = ok && mbar_poll(&p_half[t], np[t] & 1, err, 4096);
               if (!ok) break;
               issue_PV(t, sv, 0, j == 0);
               ok = mbar_poll(&p_full[t], np[t] & 1, err, 512);
@@ -529,16 +578,23 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
               issue_PV(t, sv, 1, false);
               ++np[t];
               if (j + 1 < n[t]) {
+                if (dual) {
+                  tc::commit(&kv_empty[sv]);
+                  take(sk);
+                  if (!ok) break;
+                }
                 issue_S(t, sk);
                 if (j + 2 == n[t]) tc::commit(&q_empty[t]);   // Q_t is not needed any more
+                if (dual) tc::commit(&kv_empty[sk]);
               } else {
                 tc::commit(&o_done[t]);
+                if (dual) tc::commit(&kv_empty[sv]);
               }
             }
             // Tile 0 is through with the unit: its first product of the next one goes ahead of tile
             // 1's last, if everything for it is there.
-            if (ok && t == 0 && j + 1 == nt && mbar_test(&unit_full[(i + 1) & 1], ((i + 1) >> 1) & 1)) {
-              const int n0 = units[(i + 1) & 1].n0;
+            if (ok && t == 0 && !dual && j + 1 == nt && mbar_test(&unit_full[(i + 1) & 1], ((i + 1) >> 1) & 1)) {
+              const int n0 = units[(i + 1) & 1].n[0];
               if (units[(i + 1) & 1].kind != kEnd && n0 > 0 && mbar_test(&kv_full[st], ph) && mbar_test(&q_full[0], nq[0] & 1)) {
                 tc::fence_after();
                 ++nq[0];
@@ -548,9 +604,22 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
               }
             }
           }
-          tc::commit(&kv_empty[sv]);
-          if (j + 1 < nt) tc::commit(&kv_empty[sk]);
+          if (!dual) {
+            tc::commit(&kv_empty[sv]);
+            if (j + 1 < nt) tc::commit(&kv_empty[sk]);
+          }
         }
+      };
+      for (int i = 0; ok; ++i) {
+        ok = tc::mbar_wait(&unit_full[i & 1], (i >> 1) & 1, err, 1);
+        if (!ok) break;
+        const bool end = units[i & 1].kind == kEnd, two = units[i & 1].dual;
+        const int n[2] = {units[i & 1].n[0], units[i & 1].n[1]};
+        tc::mbar_arrive(&unit_empty[i & 1]);
+        if (end) break;
+        if (max(n[0], n[1]) == 0) continue;
+        if (kPrefix && two) issue_unit(std::true_type{}, i, n);
+        else issue_unit(std::false_type{}, i, n);
       }
     }
     __syncwarp();
@@ -559,25 +628,30 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const int t = warp >> 2, row = 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + col_S(t) + lanes, tO = tmem + col_O(t) + lanes;
-    const int rpos = t * npos + (row & (npos - 1)), rhead = row >> (7 - a.gp_shift);
-    Unit w;
+    const int rhead = row >> (7 - a.gp_shift), rpos = row & (npos - 1);
     int ns = 0, nu = 0;   // S tiles and units taken
     bool ok = true;
-    for (int i = 0; ok && next_unit(i, w); ++i) {
-      const int n = t ? w.n1 : w.n0;
-      const bool row_ok = rpos < w.left;
-      const int pos = w.pos0 + rpos, head = w.h0 + rhead;
+    for (int i = 0; ok; ++i) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&unit_full[i & 1], (i >> 1) & 1, err, 1));
+      if (!ok) break;
+      const Unit& w = units[i & 1];
+      const int kind = w.kind, n = w.n[t], k0 = w.k0[t], kend = w.kend[t], tree_tile = w.tree[t], left = w.left[t];
+      const int pos = w.pos0[t] + rpos, head = w.h0[t] + rhead, base = w.base[t], part_no = w.part[t];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&unit_empty[i & 1]);
+      if (kind == kEnd) break;
+      const bool row_ok = rpos < left;
       // keys below `limit` are visible to this row
-      int limit = w.kend;
+      int limit = kend;
       uint64_t word0 = 0, word1 = 0;
       if (!kPrefix) {
-        limit = pos - w.base + 1;
+        limit = pos - base + 1;
       } else if (row_ok) {
         const int b = pos / a.N;
-        if (w.kind == kShared) {
+        if (kind == kShared) {
           const int Lb = a.L[b];
-          limit = (Lb >= 0 && Lb <= a.L_cap - a.N) ? min(Lb, w.kend) : 0;
-        } else if (w.tree >= 0) {
+          limit = (Lb >= 0 && Lb <= a.L_cap - a.N) ? min(Lb, kend) : 0;
+        } else if (tree_tile >= 0) {
           word0 = a.bits[2 * (pos - b * a.N)];
           word1 = a.bits[2 * (pos - b * a.N) + 1];
         }
@@ -594,16 +668,18 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + 32 * c, v + 32 * c);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_landed32(v + 32 * c);
-          const int vis = limit - (w.k0 + j * kKeys);
-          const bool tree = kPrefix && j == w.tree, masked = tree || __any_sync(0xffffffffu, vis < kKeys);
-          auto mask64 = [&](uint32_t* x, int c0, uint64_t word) {   // scores of the keys [c0, c0 + 64) of the tile
+          const int vis = limit - (k0 + j * kKeys);
+          const bool tree = kPrefix && j == tree_tile, masked = tree || __any_sync(0xffffffffu, vis < kKeys);
+          if (masked) {   // a bit per key, so that one piece of code masks the tree's tiles and the others
+            uint32_t see[4] = {(uint32_t)word0, (uint32_t)(word0 >> 32), (uint32_t)word1, (uint32_t)(word1 >> 32)};
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (tree ? !((word >> c) & 1ull) : c0 + c >= vis) x[c] = __float_as_uint(-INFINITY);
-          };
-          if (masked) {
-            mask64(v, 0, word0);
-            mask64(v + 64, 64, word1);
+            for (int c = 0; c < 4; ++c) {
+              const int here = vis - 32 * c;
+              if (!tree) see[c] = here >= 32 ? 0xffffffffu : here <= 0 ? 0u : (1u << here) - 1u;
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                v[32 * c + x] = (see[c] >> x) & 1u ? v[32 * c + x] : __float_as_uint(-INFINITY);
+            }
           }
           // The first 64 weights with the maximum as it stands, while the tile's own is found;
           // again only where it has to move (and at the first tile).
@@ -674,7 +750,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       // a store instruction writes 64 bytes of each row, not 16 (a quarter of the memory lines).
       const int quad = lane & 3;
       const size_t orow = (size_t)pos * a.Hq + head, orow0 = (size_t)(pos - quad) * a.Hq + head;
-      const int rows_here = w.left - (rpos - quad);   // rows of the four that exist, if positive
+      const int rows_here = left - (rpos - quad);   // rows of the four that exist, if positive
       if (!kPrefix) {
         const float inv = l_run > 0.f ? 1.f / l_run : l_run;   // (a NaN sum stays NaN)
 #pragma unroll 1
@@ -693,7 +769,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
               *reinterpret_cast<uint4*>(op + (size_t)k * a.Hq * kD) = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
         }
       } else {
-        const size_t part = (size_t)w.part * a.T * a.Hq;
+        const size_t part = (size_t)part_no * a.T * a.Hq;
         if (n > 0) {
 #pragma unroll 1
           for (int c = 0; c < kD / 32; ++c) {
@@ -760,6 +836,165 @@ rows_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
+// A few rows per KV head (single tokens): a sequence's own keys and tree, then the merge with the
+// parts of the shared rows, one CTA of 8 half-warps per (sequence, KV head). Bound by the K/V
+// bytes of the own rows: 16 lanes read a key's 256 bytes, each half-warp X keys at a time with the
+// next X on their way, and keep R rows of q and O in registers (8 head dims per lane). A tensor-core unit per (sequence,
+// KV head) would spend its time on barriers: 24 tokens of 40 heads behind 4096 rows 56 us, so
+// TAIL_US us. R: the rows, N * G, rounded up to a power of two.
+constexpr int kTailThreads = 128, kTailStreams = kTailThreads / 16, kTailRows = 8;
+
+template <int R, int X>
+__global__ void __launch_bounds__(kTailThreads)
+prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ Kp, const uint16_t* __restrict__ Vp,
+                   const uint16_t* __restrict__ Kt, const uint16_t* __restrict__ Vt, const RowsArgs a,
+                   uint16_t* __restrict__ O) {
+  constexpr int D = kPrefixD;
+  __shared__ float sm_o[kTailStreams][R][D], sm_m[kTailStreams][R], sm_l[kTailStreams][R];
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv, G = a.Hq / a.Hkv, NG = a.N * G;
+  const int stream = threadIdx.x >> 4, sub = threadIdx.x & 15;
+  const int Lb = a.L[b];
+  const bool ok = Lb >= 0 && Lb <= a.L_cap - a.N;
+  const int own = ok ? max(0, Lb - a.shared) : 0, keys = ok ? own + a.N : 0;
+  const size_t row0 = (size_t)b * a.N * a.Hq + kvh * G;   // row r: + r / G * Hq + r % G
+
+  auto unpack8 = [](const uint4& x, float* f) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(w[i]);
+      f[2 * i + 1] = bf16_hi(w[i]);
+    }
+  };
+  // A step is kStep keys, X per stream; as page_rows and shared are multiples of 128, a step's own
+  // rows lie in one page, whose id is fetched two steps ahead.
+  constexpr int kStep = kTailStreams * X;
+  static_assert(128 % kStep == 0, "a step must not cross a page");
+  auto page_of = [&](int k0) { return k0 < own ? a.table[(size_t)b * a.max_pages + (a.shared + k0) / a.page_rows] : -1; };
+  uint4 kr[X], vr[X];
+  auto fetch = [&](int k0, int page) {
+    const bool in_pool = page >= 0 && page < a.num_pages;
+    MEDUSA_CHECK(k0 >= own || in_pool, MEDUSA_CHECK_PAGE);
+    const size_t own_at = (((size_t)(in_pool ? page : 0) * a.Hkv + kvh) * a.page_rows + (a.shared + k0) % a.page_rows) * D + 8 * sub;
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      const int i = stream * X + x, key = k0 + i;
+      const uint16_t *kp = nullptr, *vp = nullptr;
+      if (key < own) {
+        if (in_pool) {   // (outside the pool: zeros, as the tensor-core path reads)
+          kp = Kp + own_at + (size_t)i * D;
+          vp = Vp + own_at + (size_t)i * D;
+        }
+      } else if (key < keys) {
+        const size_t at = (((size_t)b * a.Hkv + kvh) * a.N + key - own) * D + 8 * sub;
+        kp = Kt + at;
+        vp = Vt + at;
+      }
+      kr[x] = kp ? *reinterpret_cast<const uint4*>(kp) : make_uint4(0, 0, 0, 0);
+      vr[x] = kp ? *reinterpret_cast<const uint4*>(vp) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  int page = page_of(kStep);
+  fetch(0, page_of(0));
+  float q[R][8], o[R][8], m[R], l[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+    if (r < NG) unpack8(*reinterpret_cast<const uint4*>(Q + (row0 + (size_t)(r / G) * a.Hq + r % G) * D + 8 * sub), q[r]);
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      q[r][d] = r < NG ? q[r][d] * a.scale_log2 : 0.f;
+      o[r][d] = 0.f;
+    }
+  }
+  // (every lane of a warp takes every step: the reductions are collective)
+  for (int k0 = 0; k0 < keys; k0 += kStep) {
+    float k[X][8], v[X][8];
+    int node[X];   // -2: no key, -1: an own row, else the tree node
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      const int key = k0 + stream * X + x;
+      node[x] = key >= keys ? -2 : key < own ? -1 : key - own;
+      unpack8(kr[x], k[x]);
+      unpack8(vr[x], v[x]);
+    }
+    const int next = page;
+    page = page_of(k0 + 2 * kStep);
+    fetch(k0 + kStep, next);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float s[X], mt = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        float t = 0.f;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) t = fmaf(q[r][d], k[x][d], t);
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
+        bool see = node[x] >= -1 && r < NG;
+        if (see && node[x] >= 0) see = (a.bits[2 * (r / G) + (node[x] >> 6)] >> (node[x] & 63)) & 1ull;
+        s[x] = see ? t : -INFINITY;
+        mt = fmaxf(mt, s[x]);
+        if (!see) s[x] = -INFINITY;
+      }
+      const float mn = fmaxf(m[r], mt), mu = mn == -INFINITY ? 0.f : mn;
+      const float corr = exp2f(m[r] - mu);
+      m[r] = mn;
+      l[r] *= corr;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[r][d] *= corr;
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        const float p = exp2f(s[x] - mu);
+        l[r] += p;
+        if (s[x] != -INFINITY) {   // what is masked may hold anything
+#pragma unroll
+          for (int d = 0; d < 8; ++d) o[r][d] = fmaf(p, v[x][d], o[r][d]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d) sm_o[stream][r][8 * sub + d] = o[r][d];
+    if (sub == 0) {
+      sm_m[stream][r] = m[r];
+      sm_l[stream][r] = l[r];
+    }
+  }
+  __syncthreads();
+  const int64_t rows = (int64_t)a.T * a.Hq;
+  const int d = threadIdx.x;   // head dim
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (r >= NG) break;
+    const size_t row = row0 + (size_t)(r / G) * a.Hq + r % G;
+    float M = -INFINITY;
+    for (int x = 0; x < kTailStreams; ++x) M = fmaxf(M, sm_m[x][r]);
+    for (int x = 0; x < a.splits_s; ++x) M = fmaxf(M, a.ml_part[2 * (x * rows + row)]);
+    float acc = 0.f, sum = 0.f;
+    auto add = [&](float pm, float pl, float po) {
+      const float w = exp2f(pm - M);
+      sum += w * pl;
+      acc += w * po;
+    };
+    for (int x = 0; x < kTailStreams; ++x)
+      if (!(sm_m[x][r] == -INFINITY && sm_l[x][r] == 0.f)) add(sm_m[x][r], sm_l[x][r], sm_o[x][r][d]);
+    for (int x = 0; x < a.splits_s; ++x) {
+      const float pm = a.ml_part[2 * (x * rows + row)], pl = a.ml_part[2 * (x * rows + row) + 1];
+      if (!(pm == -INFINITY && pl == 0.f)) add(pm, pl, a.o_part[(x * rows + row) * D + d]);
+    }
+    const float out = (ok && sum != 0.f) ? acc / sum : 0.f;
+    uint16_t h;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(out));
+    O[row * D + d] = h;
+  }
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
@@ -791,32 +1026,40 @@ int gp_shift_of(int G) {
   return s;
 }
 
-// How the key ranges are split: while all units fit one wave, one CTA per SM.
+// How the key ranges are split: while all units fit one wave, one CTA per SM. Rows that fill one
+// tile go two pieces to a unit.
 struct PrefixPlan {
-  int gp_shift, splits_s, chunk_s, splits_u, chunk_u;
-  size_t o_part, ml_part, total;
+  int gp_shift, parts, tail;
+  int units_s, splits_s, chunk_s, dual_s, units_u, splits_u, chunk_u, dual_u;
+  size_t ml_part, total;
 };
 PrefixPlan plan_prefix(const medusa_cfg& c, int shared) {
   PrefixPlan p{};
   const TreeShape ts = tree_shape(c);
   p.gp_shift = gp_shift_of(c.Hq / c.Hkv);
-  const int per = 2 * (kRows >> p.gp_shift), HG = c.Hq >> p.gp_shift;
-  const int64_t us = (((int64_t)c.B * ts.N + per - 1) / per) * HG, uo = (int64_t)c.B * HG * ((ts.N + per - 1) / per);
-  auto split = [](int64_t units, int64_t keys, int* splits, int* chunk) {
-    int64_t want = kSms / units, most = (keys + 255) / 256;   // at least two tiles each
+  const int npos = kRows >> p.gp_shift, HG = c.Hq >> p.gp_shift;
+  auto split = [&](int64_t groups, int64_t positions, int64_t keys, int* units, int* splits, int* chunk, int* dual) {
+    *dual = positions <= npos;
+    const int64_t tiles = groups * ((positions + 2 * npos - 1) / (2 * npos));   // units of one key range; pieces, if dual
+    int64_t want = (*dual ? 2 : 1) * kSms / tiles, most = (keys + 255) / 256;   // at least two key tiles each
     if (want > most) want = most;
     if (want > 32) want = 32;
     if (want < 1) want = 1;
     *chunk = (int)(keys > 0 ? ((keys + want - 1) / want + kKeys - 1) / kKeys * kKeys : kKeys);
     *splits = (int)(keys > 0 ? (keys + *chunk - 1) / *chunk : 1);
+    const int64_t all = tiles * *splits;
+    *units = (int)(*dual ? (all + 1) / 2 : all);
   };
-  split(us, shared, &p.splits_s, &p.chunk_s);
-  if (shared == 0) p.splits_s = 0;
+  split(HG, (int64_t)c.B * ts.N, shared, &p.units_s, &p.splits_s, &p.chunk_s, &p.dual_s);
+  if (shared == 0) p.units_s = p.splits_s = 0;
   const int own = c.L_cap - ts.N - shared;
-  split(uo, own > 0 ? own : 0, &p.splits_u, &p.chunk_u);
-  const size_t rows = (size_t)c.B * ts.N * c.Hq, parts = p.splits_s + p.splits_u;
-  p.ml_part = align_up(parts * rows * kPrefixD * 4, 256);
-  p.total = p.ml_part + align_up(parts * rows * 8, 256);
+  // a few rows per KV head, and enough (sequence, KV head) pairs to keep every SM reading
+  p.tail = ts.N * (c.Hq / c.Hkv) <= kTailRows && (int64_t)c.B * c.Hkv >= kSms;
+  if (!p.tail) split((int64_t)c.B * HG, ts.N, own > 0 ? own : 0, &p.units_u, &p.splits_u, &p.chunk_u, &p.dual_u);
+  p.parts = p.splits_s + p.splits_u;
+  const size_t rows = (size_t)c.B * ts.N * c.Hq;
+  p.ml_part = align_up(p.parts * rows * kPrefixD * 4, 256);
+  p.total = p.ml_part + align_up(p.parts * rows * 8, 256);
   return p;
 }
 
@@ -888,14 +1131,18 @@ cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const vo
   a.max_pages = c.L_cap / page_rows;
   a.num_pages = num_pages;
   a.shared = shared;
+  a.units_s = p.units_s;
   a.splits_s = p.splits_s;
   a.chunk_s = p.chunk_s;
+  a.dual_s = p.dual_s;
+  a.units_u = p.units_u;
   a.splits_u = p.splits_u;
   a.chunk_u = p.chunk_u;
+  a.dual_u = p.dual_u;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)kPrefixD));
   a.o_part = static_cast<float*>(ws);
   a.ml_part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.ml_part);
-  const int npos = kRows >> a.gp_shift, per = 2 * npos, HG = c.Hq >> a.gp_shift;
+  const int npos = kRows >> a.gp_shift;
   const uint64_t planes = (uint64_t)num_pages * c.Hkv, tplanes = (uint64_t)c.B * c.Hkv;
   CUtensorMap m[5];
   if (!encode_3d(&m[0], kPrefixD, Q, a.T, c.Hq, (uint64_t)c.Hq * kPrefixD * 2, kPrefixD * 2, npos, 1u << a.gp_shift) ||
@@ -904,13 +1151,24 @@ cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const vo
       !encode_3d(&m[3], kPrefixD, Kt, ts.N, tplanes, kPrefixD * 2, (uint64_t)ts.N * kPrefixD * 2, kKeys, 1) ||
       !encode_3d(&m[4], kPrefixD, Vt, ts.N, tplanes, kPrefixD * 2, (uint64_t)ts.N * kPrefixD * 2, kKeys, 1))
     return cudaErrorInvalidValue;
-  const int64_t units = (int64_t)p.splits_s * HG * ((a.T + per - 1) / per) +
-                        (int64_t)p.splits_u * c.B * HG * ((ts.N + per - 1) / per);
-  cudaError_t e = launch_rows<kPrefixD, true>(m, a, units, st);
-  if (e != cudaSuccess) return e;
+  if (p.units_s + p.units_u > 0) {
+    const cudaError_t e = launch_rows<kPrefixD, true>(m, a, p.units_s + p.units_u, st);
+    if (e != cudaSuccess) return e;
+  }
+  cudaError_t e;
+  if (p.tail) {
+    const int R = ts.N * (c.Hq / c.Hkv);
+    const auto kernel = R == 1 ? prefix_tail_kernel<1, 4>
+                               : R == 2 ? prefix_tail_kernel<2, 4> : R <= 4 ? prefix_tail_kernel<4, 4> : prefix_tail_kernel<8, 2>;
+    e = launch_pdl(kernel, (unsigned)(c.B * c.Hkv), kTailThreads, 0, st, static_cast<const uint16_t*>(Q),
+                   static_cast<const uint16_t*>(Kp), static_cast<const uint16_t*>(Vp), static_cast<const uint16_t*>(Kt),
+                   static_cast<const uint16_t*>(Vt), a, static_cast<uint16_t*>(O));
+    note_launches(1);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
   const int64_t rows = (int64_t)a.T * c.Hq;
   e = launch_pdl(rows_merge_kernel, (unsigned)((rows * 32 + 255) / 256), 256, 0, st, static_cast<const float*>(a.o_part),
-                 static_cast<const float*>(a.ml_part), rows, p.splits_s + p.splits_u, static_cast<uint16_t*>(O));
+                 static_cast<const float*>(a.ml_part), rows, p.parts, static_cast<uint16_t*>(O));
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

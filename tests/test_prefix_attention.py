@@ -118,6 +118,22 @@ def test_batches(B, branching, Hq, Hkv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("branching,Hq,Hkv", [((1,), 8, 8), ((1,), 16, 8), ((1,), 24, 8), ((1,), 64, 8), ((2, 2), 8, 8),
+                                              ((3, 2, 2), 8, 8)])
+@pytest.mark.parametrize("shared", [0, 512])
+def test_few_rows_many_sequences(shared, branching, Hq, Hkv):
+    """Single tokens and small trees of enough sequences to fill the GPU (lengths on both sides of the
+    shared rows, invalid ones among them, pages that no sequence may read poisoned)."""
+    dev = gpu_ready()
+    L = [(shared - 3 + 29 * b) if b % 7 else 29 * b for b in range(25)]
+    L[3], L[11], L[12] = -1, shared, 10 ** 6
+    c = Case([min(n, 5000) for n in L], shared, 128, Hq, Hkv, branching, dev, seed=Hq + shared, poison=True, L_cap=1536)
+    O = c.call()
+    assert bool((O[3] == 0).all()) and bool((O[12] == 0).all())
+    c.check(O)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("branching", [(1,), (4, 3, 2, 1)], ids=str)
 def test_page_ids_outside_the_pool(branching):
     """A table entry outside the pool reads no memory outside it; the other sequences are right."""
