@@ -3,13 +3,16 @@
 // O = softmax(q.k / sqrt(D)) v, 64 rows of one head against tiles of 64 keys, with the
 // running maximum and sum of "최적화 2편" (beengineer500), section 3.3; everything float32.
 // Bound by the float32 multiply-adds (128 per SM and clock): 4 rows keys D operations. A
-// thread owns 4 rows x 4 keys of the scores and 4 rows x D / 16 head dims of O, so that four
-// head dims (or keys) cost 8 shared-memory words of 16 bytes for 64 multiply-adds, 12
-// bank-conflict-free wavefronts per warp; rows of Q, K and P are padded by 16 bytes for that.
-// K_{j+1} arrives while tile j's weights and values are worked on, V_j while its scores are.
-// Two groups of 256 threads take the unit's even and odd key tiles, each with its own
-// maximum, sum and O, and merge at the end: a causal prompt's last rows are its longest
-// chain, and this halves it.
+// thread owns 8 rows x 4 keys of the scores and 8 rows x D / 16 head dims of O, so that four
+// head dims (or keys) cost it 12 shared-memory words of 16 bytes, 16 wavefronts of its warp,
+// for 128 multiply-adds (4 x 4: 12 for 64, and bound by shared memory: 155 us for prompts of
+// 700, 1, 129 and 1500 tokens with 8 heads of 64, so 114 us). Rows of Q, K and P are padded
+// by 16 bytes, and a thread's rows lie 8 apart, so that no two of a warp's words meet in a
+// bank. K_{j+1} arrives while tile j's weights and values are worked on, V_j while its scores
+// are. Groups of 128 threads (4 with D = 64, 2 with D = 128, as many as shared memory holds
+// tiles for) take the unit's key tiles in turn, each with its own maximum, sum and O, and
+// merge at the end: a causal prompt's last rows are its longest chain. One CTA per unit and
+// SM, those with the most keys first.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -20,21 +23,21 @@
 namespace medusa {
 namespace {
 
-constexpr int kTileRows = 64, kTileKeys = 64;
-constexpr int kGroup = 256, kGroups = 2;
-constexpr int kThreadsF32 = kGroup * kGroups;
+constexpr int kTileRows = 64, kTileKeys = 64, kGroup = 128;
 
 template <int D>
 struct Smem {
-  static constexpr int kLd = D + 4;            // padded row of Q and K (floats)
-  static constexpr int kLdP = kTileKeys + 4;   // padded row of P
-  static constexpr int q = 0;
-  static constexpr int k = q + kTileRows * kLd;
-  static constexpr int v = k + kTileKeys * kLd;
+  static constexpr int groups = D == 64 ? 4 : 2;
+  static constexpr int threads = groups * kGroup;
+  static constexpr int ld = D + 4;            // padded row of Q and K (floats)
+  static constexpr int ldp = kTileKeys + 4;   // padded row of P
+  static constexpr int k = kTileRows * ld;    // behind Q: K, V and P of each group
+  static constexpr int v = k + kTileKeys * ld;
   static constexpr int p = v + kTileKeys * D;
-  static constexpr int per_group = p + kTileRows * kLdP - k;   // K, V and P, once per group
-  static constexpr int bytes = (k + kGroups * per_group) * 4;
-  static_assert(kTileRows * (D + 2) <= per_group, "the second group's result must fit its tiles");
+  static constexpr int per_group = p + kTileRows * ldp - k;
+  static constexpr int bytes = (k + groups * per_group) * 4;
+  static_assert(kTileRows * (D + 2) <= per_group, "a group's result must fit its tiles");
+  static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
 };
 
 __device__ __forceinline__ void cp16(float* dst, const float* src, bool valid) {
@@ -45,13 +48,12 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N)); }
 
-// 64 rows of `stride` floats from src into rows of ld floats, by thread `tid` of a group;
-// rows past `live` become zeros.
+// 64 rows of `stride` floats from src into rows of ld floats, by thread `tid` of `threads`; rows
+// past `live` become zeros.
 template <int D>
-__device__ __forceinline__ void load_tile(float* dst, int ld, const float* src, int64_t stride, int live, int tid) {
+__device__ __forceinline__ void load_tile(float* dst, int ld, const float* src, int64_t stride, int live, int tid, int threads) {
   constexpr int CH = D / 4;
-#pragma unroll
-  for (int e = tid; e < 64 * CH; e += kGroup) {
+  for (int e = tid; e < 64 * CH; e += threads) {
     const int r = e / CH, c = e % CH;
     const bool ok = r < live;
     cp16(dst + r * ld + 4 * c, src + (ok ? r : 0) * stride + 4 * c, ok);
@@ -59,7 +61,7 @@ __device__ __forceinline__ void load_tile(float* dst, int ld, const float* src, 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreadsF32, 1)
+__global__ void __launch_bounds__(Smem<D>::threads, 1)
 prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V, int T, int64_t qs,
                   int64_t ks, int64_t vs, const int32_t* __restrict__ cu, int B, int Hq, int Hkv, float scale_log2,
                   float* __restrict__ O) {
@@ -70,170 +72,181 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
   extern __shared__ __align__(16) float smem[];
   __shared__ int unit_b, unit_t;
   const int group = threadIdx.x / kGroup, tid = threadIdx.x % kGroup;
-  float *sq = smem + S::q, *sk = smem + S::k + group * S::per_group, *sv = sk + S::v - S::k, *sp = sk + S::p - S::k;
-  const int rg = tid >> 4, cg = tid & 15;   // rows 4 rg .., keys cg + 16 i, head dims 4 cg + 64 n ..
+  float *sq = smem, *sk = smem + S::k + group * S::per_group, *sv = sk + S::v - S::k, *sp = sk + S::p - S::k;
+  const int rg = tid >> 4, cg = tid & 15;   // rows rg + 8 i, keys cg + 16 c, head dims 4 cg + 64 n ..
   auto sync_group = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroup) : "memory"); };
-  PromptWalk walk;
-  if (threadIdx.x < 32) walk.begin(cu, B, T, kTileRows);
 
-  for (int64_t u = blockIdx.x;; u += gridDim.x) {
-    if (threadIdx.x < 32) {
-      const int b = walk.find((int)(u / Hq));
-      if (threadIdx.x == 0) {
-        unit_b = b;
-        unit_t = walk.t;
-      }
+  if (threadIdx.x < 32) {
+    PromptWalk walk;
+    walk.begin(cu, B, T, kTileRows);
+    const int b = walk.find((int)(blockIdx.x / Hq));
+    if (threadIdx.x == 0) {
+      unit_b = b;
+      unit_t = walk.t;
     }
-    __syncthreads();
-    const int b = unit_b, r0 = unit_t * kTileRows;
-    if (b < 0) break;
-    const int h = (int)(u % Hq), kvh = h / (Hq / Hkv);
-    const int64_t c0 = cu[b];
-    const int len = cu[b + 1] - (int)c0, rows = min(kTileRows, len - r0), keys = r0 + rows;
-    const int nt = (keys + kTileKeys - 1) / kTileKeys;
-    const float* kp = K + c0 * ks + (size_t)kvh * D;
-    const float* vp = V + c0 * vs + (size_t)kvh * D;
-    if (group == 0) load_tile<D>(sq, S::kLd, Q + (c0 + r0) * qs + (size_t)h * D, qs, rows, tid);
-    if (group < nt) load_tile<D>(sk, S::kLd, kp + (int64_t)group * kTileKeys * ks, ks, keys - group * kTileKeys, tid);
+  }
+  __syncthreads();
+  const int b = unit_b, r0 = unit_t * kTileRows;
+  if (b < 0) return;   // (the grid may hold more blocks than there are units)
+  const int h = (int)(blockIdx.x % Hq), kvh = h / (Hq / Hkv);
+  const int64_t c0 = cu[b];
+  const int len = cu[b + 1] - (int)c0, rows = min(kTileRows, len - r0), keys = r0 + rows;
+  const int nt = (keys + kTileKeys - 1) / kTileKeys;
+  const float* kp = K + c0 * ks + (size_t)kvh * D;
+  const float* vp = V + c0 * vs + (size_t)kvh * D;
+  load_tile<D>(sq, S::ld, Q + (c0 + r0) * qs + (size_t)h * D, qs, rows, threadIdx.x, S::threads);
+  if (group < nt) load_tile<D>(sk, S::ld, kp + (int64_t)group * kTileKeys * ks, ks, keys - group * kTileKeys, tid, kGroup);
+  cp_commit();
+
+  float4 o[8][NC];
+  float m[8], l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) o[i][n] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  cp_wait<0>();
+  __syncthreads();       // Q
+  for (int j = group; j < nt; j += S::groups) {
+    const int k0 = j * kTileKeys;
+    cp_wait<0>();        // K_j
+    sync_group();        // ... of every thread; V and P of the tile before are no longer read
+    load_tile<D>(sv, D, vp + k0 * vs, vs, keys - k0, tid, kGroup);
     cp_commit();
-
-    float4 o[4][NC];
-    float m[4], l[4];
+    float s[8][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int n = 0; n < NC; ++n) o[i][n] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    cp_wait<0>();
-    __syncthreads();       // Q of group 0
-    for (int j = group; j < nt; j += kGroups) {
-      const int k0 = j * kTileKeys;
-      cp_wait<0>();        // K_j
-      sync_group();        // ... of every thread; V and P of the tile before are no longer read
-      load_tile<D>(sv, D, vp + k0 * vs, vs, keys - k0, tid);
-      cp_commit();
-      float2 s[4][4];   // (even, odd) head dims
+      for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
+#pragma unroll 2
+    for (int d = 0; d < D; d += 4) {
+      float4 w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const float4*>(sk + (cg + 16 * c) * S::ld + d);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[i][c] = make_float2(0.f, 0.f);
-#pragma unroll 4
-      for (int d = 0; d < D; d += 4) {
-        float4 a[4], w[4];
+      for (int i = 0; i < 8; ++i) {
+        const float4 a = *reinterpret_cast<const float4*>(sq + (rg + 8 * i) * S::ld + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (4 * rg + i) * S::kLd + d);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const float4*>(sk + (cg + 16 * c) * S::kLd + d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            s[i][c] = __ffma2_rn(make_float2(a[i].x, a[i].y), make_float2(w[c].x, w[c].y), s[i][c]);
-            s[i][c] = __ffma2_rn(make_float2(a[i].z, a[i].w), make_float2(w[c].z, w[c].w), s[i][c]);
-          }
+        for (int c = 0; c < 4; ++c) {
+          s[i][c] = fmaf(a.x, w[c].x, s[i][c]);
+          s[i][c] = fmaf(a.y, w[c].y, s[i][c]);
+          s[i][c] = fmaf(a.z, w[c].z, s[i][c]);
+          s[i][c] = fmaf(a.w, w[c].w, s[i][c]);
+        }
       }
-      sync_group();        // K_j is no longer read
-      constexpr int ahead = kGroups * kTileKeys;
-      if (j + kGroups < nt) load_tile<D>(sk, S::kLd, kp + (int64_t)(k0 + ahead) * ks, ks, keys - k0 - ahead, tid);
-      cp_commit();
+    }
+    sync_group();        // K_j is no longer read
+    constexpr int ahead = S::groups * kTileKeys;
+    if (j + S::groups < nt) load_tile<D>(sk, S::ld, kp + (int64_t)(k0 + ahead) * ks, ks, keys - k0 - ahead, tid, kGroup);
+    cp_commit();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int see = r0 + 4 * rg + i - k0;   // keys 0..see of the tile are visible to the row
-        float x[4], mt = -INFINITY;
+    for (int i = 0; i < 8; ++i) {
+      const int see = r0 + rg + 8 * i - k0;   // keys 0..see of the tile are visible to the row
+      float x[4], mt = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          x[c] = cg + 16 * c <= see ? (s[i][c].x + s[i][c].y) * scale_log2 : -INFINITY;
-          mt = fmaxf(mt, x[c]);
-        }
+      for (int c = 0; c < 4; ++c) {
+        x[c] = cg + 16 * c <= see ? s[i][c] * scale_log2 : -INFINITY;
+        mt = fmaxf(mt, x[c]);
+      }
 #pragma unroll
-        for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, w));   // the row's 16 threads
-        const float mn = fmaxf(m[i], mt), mu = mn == -INFINITY ? 0.f : mn;
-        const float corr = exp2f(m[i] - mu);
-        m[i] = mn;
-        float ps = 0.f;
+      for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, w));   // the row's 16 threads
+      const float mn = fmaxf(m[i], mt), mu = mn == -INFINITY ? 0.f : mn;
+      const float corr = exp2f(m[i] - mu);
+      m[i] = mn;
+      float ps = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float p = exp2f(x[c] - mu);
-          ps += p;
-          sp[(4 * rg + i) * S::kLdP + cg + 16 * c] = p;
-        }
-        l[i] = l[i] * corr + ps;
+      for (int c = 0; c < 4; ++c) {
+        const float p = exp2f(x[c] - mu);
+        ps += p;
+        sp[(rg + 8 * i) * S::ldp + cg + 16 * c] = p;
+      }
+      l[i] = l[i] * corr + ps;
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        o[i][n].x *= corr;
+        o[i][n].y *= corr;
+        o[i][n].z *= corr;
+        o[i][n].w *= corr;
+      }
+    }
+    cp_wait<1>();        // V_j
+    sync_group();        // ... and P_j
+#pragma unroll 2
+    for (int k = 0; k < kTileKeys; k += 4) {
+      float4 w[4][NC];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) w[x][n] = *reinterpret_cast<const float4*>(sv + (k + x) * D + 64 * n + 4 * cg);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 p = *reinterpret_cast<const float4*>(sp + (rg + 8 * i) * S::ldp + k);
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-          o[i][n].x *= corr;
-          o[i][n].y *= corr;
-          o[i][n].z *= corr;
-          o[i][n].w *= corr;
-        }
-      }
-      cp_wait<1>();        // V_j
-      sync_group();        // ... and P_j
-#pragma unroll 4
-      for (int k = 0; k < kTileKeys; k += 4) {
-        float4 p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (4 * rg + i) * S::kLdP + k);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          float4 w[NC];
-#pragma unroll
-          for (int n = 0; n < NC; ++n) w[n] = *reinterpret_cast<const float4*>(sv + (k + x) * D + 64 * n + 4 * cg);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float pv = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
-            const float2 pp = make_float2(pv, pv);
-#pragma unroll
-            for (int n = 0; n < NC; ++n) {
-              const float2 lo = __ffma2_rn(pp, make_float2(w[n].x, w[n].y), make_float2(o[i][n].x, o[i][n].y));
-              const float2 hi = __ffma2_rn(pp, make_float2(w[n].z, w[n].w), make_float2(o[i][n].z, o[i][n].w));
-              o[i][n] = make_float4(lo.x, lo.y, hi.x, hi.y);
-            }
-          }
+          float4 t = o[i][n];
+          t.x = fmaf(p.x, w[0][n].x, t.x), t.y = fmaf(p.x, w[0][n].y, t.y);
+          t.z = fmaf(p.x, w[0][n].z, t.z), t.w = fmaf(p.x, w[0][n].w, t.w);
+          t.x = fmaf(p.y, w[1][n].x, t.x), t.y = fmaf(p.y, w[1][n].y, t.y);
+          t.z = fmaf(p.y, w[1][n].z, t.z), t.w = fmaf(p.y, w[1][n].w, t.w);
+          t.x = fmaf(p.z, w[2][n].x, t.x), t.y = fmaf(p.z, w[2][n].y, t.y);
+          t.z = fmaf(p.z, w[2][n].z, t.z), t.w = fmaf(p.z, w[2][n].w, t.w);
+          t.x = fmaf(p.w, w[3][n].x, t.x), t.y = fmaf(p.w, w[3][n].y, t.y);
+          t.z = fmaf(p.w, w[3][n].z, t.z), t.w = fmaf(p.w, w[3][n].w, t.w);
+          o[i][n] = t;
         }
       }
     }
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
-    // group 1 leaves its maximum, sum and O where its tiles were; group 0 merges and stores
-    float* so = smem + S::k + S::per_group;
-    float* sml = so + kTileRows * D;
-    if (group == 1) {
-      sync_group();        // its last tile is no longer read
+    for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+  // The other groups leave their maximum, sum and O where their tiles were; group 0 merges and stores.
+  if (group > 0) {
+    sync_group();        // the group's last tile is no longer read
+    float *so = sk, *sml = so + kTileRows * D;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (cg == 0) {
-          sml[2 * (4 * rg + i)] = m[i];
-          sml[2 * (4 * rg + i) + 1] = l[i];
-        }
+    for (int i = 0; i < 8; ++i) {
+      const int r = rg + 8 * i;
+      if (cg == 0) {
+        sml[2 * r] = m[i];
+        sml[2 * r + 1] = l[i];
+      }
 #pragma unroll
-        for (int n = 0; n < NC; ++n) *reinterpret_cast<float4*>(so + (4 * rg + i) * D + 64 * n + 4 * cg) = o[i][n];
+      for (int n = 0; n < NC; ++n) *reinterpret_cast<float4*>(so + r * D + 64 * n + 4 * cg) = o[i][n];
+    }
+  }
+  cp_wait<0>();
+  __syncthreads();
+  if (group > 0) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = rg + 8 * i;
+    if (r >= rows) continue;
+    // A row saw its own key at least, so its largest maximum is no -inf (unless it is no number).
+    float M = m[i];
+    for (int g = 1; g < S::groups; ++g) M = fmaxf(M, smem[S::k + g * S::per_group + kTileRows * D + 2 * r]);
+    float w = m[i] == M ? 1.f : exp2f(m[i] - M), sum = l[i] * w;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) o[i][n] = make_float4(o[i][n].x * w, o[i][n].y * w, o[i][n].z * w, o[i][n].w * w);
+    for (int g = 1; g < S::groups; ++g) {
+      const float* so = smem + S::k + g * S::per_group;
+      const float mg = so[kTileRows * D + 2 * r];
+      w = mg == M ? 1.f : exp2f(mg - M);
+      sum += so[kTileRows * D + 2 * r + 1] * w;
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        const float4 x = *reinterpret_cast<const float4*>(so + r * D + 64 * n + 4 * cg);
+        o[i][n] = make_float4(o[i][n].x + x.x * w, o[i][n].y + x.y * w, o[i][n].z + x.z * w, o[i][n].w + x.w * w);
       }
     }
-    cp_wait<0>();
-    __syncthreads();
-    if (group == 0) {
+    const float inv = 1.f / sum;
+    float* op = O + ((size_t)(c0 + r0 + r) * Hq + h) * D + 4 * cg;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float m1 = sml[2 * (4 * rg + i)], l1 = sml[2 * (4 * rg + i) + 1], M = fmaxf(m[i], m1);
-        if (4 * rg + i < rows) {   // such a row saw its own key at least, so M is no -inf (unless it is no number)
-          const float w0 = m[i] == M ? 1.f : exp2f(m[i] - M), w1 = m1 == M ? 1.f : exp2f(m1 - M);
-          const float inv = 1.f / (l[i] * w0 + l1 * w1);
-          float* op = O + ((size_t)(c0 + r0 + 4 * rg + i) * Hq + h) * D + 4 * cg;
-#pragma unroll
-          for (int n = 0; n < NC; ++n) {
-            const float4 x = *reinterpret_cast<const float4*>(so + (4 * rg + i) * D + 64 * n + 4 * cg);
-            *reinterpret_cast<float4*>(op + 64 * n) =
-                make_float4((o[i][n].x * w0 + x.x * w1) * inv, (o[i][n].y * w0 + x.y * w1) * inv,
-                            (o[i][n].z * w0 + x.z * w1) * inv, (o[i][n].w * w0 + x.w * w1) * inv);
-          }
-        }
-      }
-    }
-    __syncthreads();   // the unit, Q and the tiles may be overwritten
+    for (int n = 0; n < NC; ++n)
+      *reinterpret_cast<float4*>(op + 64 * n) = make_float4(o[i][n].x * inv, o[i][n].y * inv, o[i][n].z * inv, o[i][n].w * inv);
   }
 }
 
@@ -244,10 +257,9 @@ cudaError_t run(const medusa_cfg& c, const void* Q, const void* K, const void* V
   cudaError_t e = cudaFuncSetAttribute(prompt_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes);
   if (e != cudaSuccess) return e;
   const int64_t units = ((int64_t)T / kTileRows + c.B) * c.Hq;   // at least as many as there are
-  const int64_t resident = 152;   // one CTA per SM
-  e = launch_pdl(prompt_f32_kernel<D>, (unsigned)(units < resident ? units : resident), kThreadsF32, Smem<D>::bytes, st,
-                 static_cast<const float*>(Q), static_cast<const float*>(K), static_cast<const float*>(V), T, qs, ks, vs, cu,
-                 c.B, c.Hq, c.Hkv, scale_log2, static_cast<float*>(O));
+  e = launch_pdl(prompt_f32_kernel<D>, (unsigned)units, Smem<D>::threads, Smem<D>::bytes, st, static_cast<const float*>(Q),
+                 static_cast<const float*>(K), static_cast<const float*>(V), T, qs, ks, vs, cu, c.B, c.Hq, c.Hkv, scale_log2,
+                 static_cast<float*>(O));
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

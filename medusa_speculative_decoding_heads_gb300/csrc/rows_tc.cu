@@ -60,7 +60,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSms = 152;
-constexpr int kAhead = 6;   // steps (K and V tiles) of a unit still to be loaded when the next unit is fetched
+constexpr int kAhead = 8;   // steps (K and V tiles) of a unit still to be loaded when the next unit is fetched
 // The running maximum moves (and O is rescaled) only when a tile's maximum exceeds it by more
 // than this many binary orders of magnitude: weights stay below 2^8, far inside bf16 and f32.
 constexpr float kLazy = 8.f;
@@ -837,20 +837,21 @@ rows_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml
 }
 
 // A few rows per KV head (single tokens): a sequence's own keys and tree, then the merge with the
-// parts of the shared rows, one CTA of 8 half-warps per (sequence, KV head). Bound by the K/V
+// parts of the shared rows, one CTA of 8 or 16 half-warps per (sequence, KV head). Bound by the K/V
 // bytes of the own rows: 16 lanes read a key's 256 bytes, each half-warp X keys at a time with the
 // next X on their way, and keep R rows of q and O in registers (8 head dims per lane). A tensor-core unit per (sequence,
 // KV head) would spend its time on barriers: 24 tokens of 40 heads behind 4096 rows 56 us, so
-// TAIL_US us. R: the rows, N * G, rounded up to a power of two.
-constexpr int kTailThreads = 128, kTailStreams = kTailThreads / 16, kTailRows = 8;
+// 47 us. R: the rows, N * G, rounded up to a power of two.
+constexpr int kTailRows = 8, kTailAhead = 1024;
 
-template <int R, int X>
+template <int R, int X, int kTailThreads>
 __global__ void __launch_bounds__(kTailThreads)
 prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ Kp, const uint16_t* __restrict__ Vp,
                    const uint16_t* __restrict__ Kt, const uint16_t* __restrict__ Vt, const RowsArgs a,
                    uint16_t* __restrict__ O) {
-  constexpr int D = kPrefixD;
-  __shared__ float sm_o[kTailStreams][R][D], sm_m[kTailStreams][R], sm_l[kTailStreams][R];
+  constexpr int D = kPrefixD, kTailStreams = kTailThreads / 16;
+  __shared__ __align__(16) float sm_o[kTailStreams][R][D];
+  __shared__ float sm_m[kTailStreams][R], sm_l[kTailStreams][R];
   pdl_trigger();
   pdl_wait();
   const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv, G = a.Hq / a.Hkv, NG = a.N * G;
@@ -860,6 +861,18 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
   const int own = ok ? max(0, Lb - a.shared) : 0, keys = ok ? own + a.N : 0;
   const size_t row0 = (size_t)b * a.N * a.Hq + kvh * G;   // row r: + r / G * Hq + r % G
 
+  // All of the own rows start for L2 at once (a row per thread), so that the steps below wait for
+  // L2 and not, one after the other, for DRAM.
+  for (int i = threadIdx.x; i < min(own, kTailAhead); i += kTailThreads) {
+    const int row = a.shared + i, page = a.table[(size_t)b * a.max_pages + row / a.page_rows];
+    if (page < 0 || page >= a.num_pages) continue;
+    const size_t at = (((size_t)page * a.Hkv + kvh) * a.page_rows + row % a.page_rows) * D;
+#pragma unroll
+    for (int x = 0; x < D; x += 64) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(Kp + at + x));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(Vp + at + x));
+    }
+  }
   auto unpack8 = [](const uint4& x, float* f) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -912,49 +925,56 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
   }
   // (every lane of a warp takes every step: the reductions are collective)
   for (int k0 = 0; k0 < keys; k0 += kStep) {
-    float k[X][8], v[X][8];
-    int node[X];   // -2: no key, -1: an own row, else the tree node
+    float s[R][X];
+    uint4 vc[X];
 #pragma unroll
     for (int x = 0; x < X; ++x) {
-      const int key = k0 + stream * X + x;
-      node[x] = key >= keys ? -2 : key < own ? -1 : key - own;
-      unpack8(kr[x], k[x]);
-      unpack8(vr[x], v[x]);
+      float k[8];
+      unpack8(kr[x], k);
+      vc[x] = vr[x];
+      const int key = k0 + stream * X + x, node = key - own;   // node >= 0: of the tree
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float t = 0.f;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) t = fmaf(q[r][d], k[d], t);
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
+        bool see = key < keys && r < NG;
+        if (see && node >= 0) see = (a.bits[2 * (r / G) + (node >> 6)] >> (node & 63)) & 1ull;
+        s[r][x] = see ? t : -INFINITY;
+      }
     }
     const int next = page;
     page = page_of(k0 + 2 * kStep);
     fetch(k0 + kStep, next);
+    float p[R][X];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float s[X], mt = -INFINITY;
+      float mn = m[r];
 #pragma unroll
-      for (int x = 0; x < X; ++x) {
-        float t = 0.f;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) t = fmaf(q[r][d], k[x][d], t);
-#pragma unroll
-        for (int w = 8; w > 0; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
-        bool see = node[x] >= -1 && r < NG;
-        if (see && node[x] >= 0) see = (a.bits[2 * (r / G) + (node[x] >> 6)] >> (node[x] & 63)) & 1ull;
-        s[x] = see ? t : -INFINITY;
-        mt = fmaxf(mt, s[x]);
-        if (!see) s[x] = -INFINITY;
-      }
-      const float mn = fmaxf(m[r], mt), mu = mn == -INFINITY ? 0.f : mn;
-      const float corr = exp2f(m[r] - mu);
+      for (int x = 0; x < X; ++x) mn = fmaxf(mn, s[r][x]);
+      const float mu = mn == -INFINITY ? 0.f : mn, corr = exp2f(m[r] - mu);
       m[r] = mn;
       l[r] *= corr;
 #pragma unroll
       for (int d = 0; d < 8; ++d) o[r][d] *= corr;
 #pragma unroll
       for (int x = 0; x < X; ++x) {
-        const float p = exp2f(s[x] - mu);
-        l[r] += p;
-        if (s[x] != -INFINITY) {   // what is masked may hold anything
-#pragma unroll
-          for (int d = 0; d < 8; ++d) o[r][d] = fmaf(p, v[x][d], o[r][d]);
-        }
+        p[r][x] = exp2f(s[r][x] - mu);
+        l[r] += p[r][x];
       }
+    }
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      float v[8];
+      unpack8(vc[x], v);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (s[r][x] != -INFINITY) {   // what is masked may hold anything
+#pragma unroll
+          for (int d = 0; d < 8; ++d) o[r][d] = fmaf(p[r][x], v[d], o[r][d]);
+        }
     }
   }
 #pragma unroll
@@ -967,31 +987,40 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
     }
   }
   __syncthreads();
+  // merge: a warp per row, 4 head dims per lane; the streams' results, then the shared rows' parts
   const int64_t rows = (int64_t)a.T * a.Hq;
-  const int d = threadIdx.x;   // head dim
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (r >= NG) break;
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < NG; r += kTailThreads / 32) {
     const size_t row = row0 + (size_t)(r / G) * a.Hq + r % G;
-    float M = -INFINITY;
-    for (int x = 0; x < kTailStreams; ++x) M = fmaxf(M, sm_m[x][r]);
-    for (int x = 0; x < a.splits_s; ++x) M = fmaxf(M, a.ml_part[2 * (x * rows + row)]);
-    float acc = 0.f, sum = 0.f;
-    auto add = [&](float pm, float pl, float po) {
-      const float w = exp2f(pm - M);
-      sum += w * pl;
-      acc += w * po;
+    float M = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float pm, float pl, const float4& po) {
+      if (pm == -INFINITY && pl == 0.f) return;   // nothing was visible: its O need not have been written
+      const float mn = fmaxf(M, pm), mu = mn == -INFINITY ? 0.f : mn, w0 = exp2f(M - mu), w1 = exp2f(pm - mu);
+      M = mn;
+      sum = sum * w0 + pl * w1;
+      acc = make_float4(acc.x * w0 + po.x * w1, acc.y * w0 + po.y * w1, acc.z * w0 + po.z * w1, acc.w * w0 + po.w * w1);
     };
-    for (int x = 0; x < kTailStreams; ++x)
-      if (!(sm_m[x][r] == -INFINITY && sm_l[x][r] == 0.f)) add(sm_m[x][r], sm_l[x][r], sm_o[x][r][d]);
-    for (int x = 0; x < a.splits_s; ++x) {
-      const float pm = a.ml_part[2 * (x * rows + row)], pl = a.ml_part[2 * (x * rows + row) + 1];
-      if (!(pm == -INFINITY && pl == 0.f)) add(pm, pl, a.o_part[(x * rows + row) * D + d]);
+    for (int x0 = 0; x0 < a.splits_s; x0 += 4) {
+      float2 ml[4];
+      float4 po[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const bool there = x0 + x < a.splits_s;
+        const size_t at = (size_t)(there ? x0 + x : 0) * rows + row;
+        ml[x] = *reinterpret_cast<const float2*>(a.ml_part + 2 * at);
+        po[x] = *reinterpret_cast<const float4*>(a.o_part + at * D + 4 * lane);
+        if (!there) ml[x] = make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) add(ml[x].x, ml[x].y, po[x]);
     }
-    const float out = (ok && sum != 0.f) ? acc / sum : 0.f;
-    uint16_t h;
-    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(out));
-    O[row * D + d] = h;
+#pragma unroll
+    for (int x = 0; x < kTailStreams; ++x)
+      add(sm_m[x][r], sm_l[x][r], *reinterpret_cast<const float4*>(&sm_o[x][r][4 * lane]));
+    const float inv = (ok && sum != 0.f) ? 1.f / sum : 0.f;
+    *reinterpret_cast<uint2*>(O + row * D + 4 * lane) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   }
 }
 
@@ -1158,9 +1187,10 @@ cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const vo
   cudaError_t e;
   if (p.tail) {
     const int R = ts.N * (c.Hq / c.Hkv);
-    const auto kernel = R == 1 ? prefix_tail_kernel<1, 4>
-                               : R == 2 ? prefix_tail_kernel<2, 4> : R <= 4 ? prefix_tail_kernel<4, 4> : prefix_tail_kernel<8, 2>;
-    e = launch_pdl(kernel, (unsigned)(c.B * c.Hkv), kTailThreads, 0, st, static_cast<const uint16_t*>(Q),
+    const auto kernel = R == 1 ? prefix_tail_kernel<1, 4, 256>
+                               : R == 2 ? prefix_tail_kernel<2, 4, 256>
+                                        : R <= 4 ? prefix_tail_kernel<4, 4, 256> : prefix_tail_kernel<8, 2, 128>;
+    e = launch_pdl(kernel, (unsigned)(c.B * c.Hkv), R <= 4 ? 256 : 128, 0, st, static_cast<const uint16_t*>(Q),
                    static_cast<const uint16_t*>(Kp), static_cast<const uint16_t*>(Vp), static_cast<const uint16_t*>(Kt),
                    static_cast<const uint16_t*>(Vt), a, static_cast<uint16_t*>(O));
     note_launches(1);
