@@ -5,14 +5,15 @@
 // Bound by the float32 multiply-adds (128 per SM and clock): 4 rows keys D operations. A
 // thread owns 8 rows x 4 keys of the scores and 8 rows x D / 16 head dims of O, so that four
 // head dims (or keys) cost it 12 shared-memory words of 16 bytes, 16 wavefronts of its warp,
-// for 128 multiply-adds (4 x 4: 12 for 64, and bound by shared memory: 155 us for prompts of
-// 700, 1, 129 and 1500 tokens with 8 heads of 64, so 114 us). Rows of Q, K and P are padded
-// by 16 bytes, and a thread's rows lie 8 apart, so that no two of a warp's words meet in a
-// bank. K_{j+1} arrives while tile j's weights and values are worked on, V_j while its scores
-// are. Groups of 128 threads (4 with D = 64, 2 with D = 128, as many as shared memory holds
-// tiles for) take the unit's key tiles in turn, each with its own maximum, sum and O, and
-// merge at the end: a causal prompt's last rows are its longest chain. One CTA per unit and
-// SM, those with the most keys first.
+// for 128 multiply-adds, issued in pairs (prompts of 700, 1, 129 and 1500 tokens, 8 heads of
+// 64: 155 us with 4 x 4 per thread, bound by shared memory; 101 us with single multiply-adds,
+// by their issue; 85 us so, 39 TFLOP/s on longer ones). Rows of Q, K and P are padded by 16
+// bytes, and a thread's rows lie 8 apart, so that no two of a warp's words meet in a bank.
+// K_{j+1} arrives while tile j's weights and values are worked on, V_j while its scores are.
+// Groups of 128 threads (3 with D = 64, 2 with D = 128: as many as registers and shared memory
+// hold tiles for) take the unit's key tiles in turn, each with its own maximum, sum and O, and
+// merge at the end: a causal prompt's last rows are its longest chain. One CTA per unit and SM,
+// those with the most keys first.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -27,7 +28,7 @@ constexpr int kTileRows = 64, kTileKeys = 64, kGroup = 128;
 
 template <int D>
 struct Smem {
-  static constexpr int groups = D == 64 ? 4 : 2;
+  static constexpr int groups = D == 64 ? 3 : 2;
   static constexpr int threads = groups * kGroup;
   static constexpr int ld = D + 4;            // padded row of Q and K (floats)
   static constexpr int ldp = kTileKeys + 4;   // padded row of P
@@ -115,11 +116,11 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
     sync_group();        // ... of every thread; V and P of the tile before are no longer read
     load_tile<D>(sv, D, vp + k0 * vs, vs, keys - k0, tid, kGroup);
     cp_commit();
-    float s[8][4];
+    float2 s[8][4];   // (even, odd) head dims
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
+      for (int c = 0; c < 4; ++c) s[i][c] = make_float2(0.f, 0.f);
 #pragma unroll 2
     for (int d = 0; d < D; d += 4) {
       float4 w[4];
@@ -129,12 +130,9 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
       for (int i = 0; i < 8; ++i) {
         const float4 a = *reinterpret_cast<const float4*>(sq + (rg + 8 * i) * S::ld + d);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          s[i][c] = fmaf(a.x, w[c].x, s[i][c]);
-          s[i][c] = fmaf(a.y, w[c].y, s[i][c]);
-          s[i][c] = fmaf(a.z, w[c].z, s[i][c]);
-          s[i][c] = fmaf(a.w, w[c].w, s[i][c]);
-        }
+        for (int c = 0; c < 4; ++c) s[i][c] = __ffma2_rn(make_float2(a.x, a.y), make_float2(w[c].x, w[c].y), s[i][c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[i][c] = __ffma2_rn(make_float2(a.z, a.w), make_float2(w[c].z, w[c].w), s[i][c]);
       }
     }
     sync_group();        // K_j is no longer read
@@ -147,7 +145,7 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
       float x[4], mt = -INFINITY;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        x[c] = cg + 16 * c <= see ? s[i][c] * scale_log2 : -INFINITY;
+        x[c] = cg + 16 * c <= see ? (s[i][c].x + s[i][c].y) * scale_log2 : -INFINITY;
         mt = fmaxf(mt, x[c]);
       }
 #pragma unroll
@@ -185,16 +183,15 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
         const float4 p = *reinterpret_cast<const float4*>(sp + (rg + 8 * i) * S::ldp + k);
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-          float4 t = o[i][n];
-          t.x = fmaf(p.x, w[0][n].x, t.x), t.y = fmaf(p.x, w[0][n].y, t.y);
-          t.z = fmaf(p.x, w[0][n].z, t.z), t.w = fmaf(p.x, w[0][n].w, t.w);
-          t.x = fmaf(p.y, w[1][n].x, t.x), t.y = fmaf(p.y, w[1][n].y, t.y);
-          t.z = fmaf(p.y, w[1][n].z, t.z), t.w = fmaf(p.y, w[1][n].w, t.w);
-          t.x = fmaf(p.z, w[2][n].x, t.x), t.y = fmaf(p.z, w[2][n].y, t.y);
-          t.z = fmaf(p.z, w[2][n].z, t.z), t.w = fmaf(p.z, w[2][n].w, t.w);
-          t.x = fmaf(p.w, w[3][n].x, t.x), t.y = fmaf(p.w, w[3][n].y, t.y);
-          t.z = fmaf(p.w, w[3][n].z, t.z), t.w = fmaf(p.w, w[3][n].w, t.w);
-          o[i][n] = t;
+          float2 lo = make_float2(o[i][n].x, o[i][n].y), hi = make_float2(o[i][n].z, o[i][n].w);
+          const float pk[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 pp = make_float2(pk[x], pk[x]);
+            lo = __ffma2_rn(pp, make_float2(w[x][n].x, w[x][n].y), lo);
+            hi = __ffma2_rn(pp, make_float2(w[x][n].z, w[x][n].w), hi);
+          }
+          o[i][n] = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
       }
     }

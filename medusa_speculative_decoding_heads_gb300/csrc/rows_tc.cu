@@ -807,33 +807,54 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 
 constexpr int kPrefixD = 128;
 
-// O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the splits; one warp per output row.
+// The merge of partial results of one row, 4 head dims per lane: O = sum_s 2^(m_s - M) o_s /
+// sum_s 2^(m_s - M) l_s.
+struct Merge {
+  float M = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(float m, float l, const float4& o) {
+    if (m == -INFINITY && l == 0.f) return;   // nothing was visible: its O need not have been written
+    const float mn = fmaxf(M, m), mu = mn == -INFINITY ? 0.f : mn, w0 = exp2f(M - mu), w1 = exp2f(m - mu);
+    M = mn;
+    sum = sum * w0 + l * w1;
+    acc = make_float4(acc.x * w0 + o.x * w1, acc.y * w0 + o.y * w1, acc.z * w0 + o.z * w1, acc.w * w0 + o.w * w1);
+  }
+  // parts [0, splits) of a row, X loads at a time
+  template <int X>
+  __device__ __forceinline__ void parts(const float* __restrict__ o_part, const float* __restrict__ ml_part, int64_t rows,
+                                        int64_t row, int splits) {
+    for (int s0 = 0; s0 < splits; s0 += X) {
+      float2 ml[X];
+      float4 o[X];
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        const int64_t at = (s0 + x < splits ? s0 + x : 0) * rows + row;
+        ml[x] = *reinterpret_cast<const float2*>(ml_part + 2 * at);
+        o[x] = *reinterpret_cast<const float4*>(o_part + at * kPrefixD + 4 * (threadIdx.x & 31));
+        if (s0 + x >= splits) ml[x] = make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int x = 0; x < X; ++x) add(ml[x].x, ml[x].y, o[x]);
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* O, int64_t row) const {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;   // no key at all: zeros
+    *reinterpret_cast<uint2*>(O + row * kPrefixD + 4 * (threadIdx.x & 31)) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  }
+};
+
+// One warp per output row. Bound by the partial results' bytes.
 __global__ void __launch_bounds__(256)
 rows_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml_part, int64_t rows, int splits,
                   uint16_t* __restrict__ O) {
   pdl_wait();
   pdl_trigger();
   const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
   if (row >= rows) return;
-  float M = -INFINITY;
-  for (int s = 0; s < splits; ++s) M = fmaxf(M, ml_part[2 * (s * rows + row)]);
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < splits; ++s) {
-    const float m = ml_part[2 * (s * rows + row)], ls = ml_part[2 * (s * rows + row) + 1];
-    if (m == -INFINITY && ls == 0.f) continue;   // nothing was visible: its O need not have been written
-    const float wgt = exp2f(m - M);
-    const float4 o = *reinterpret_cast<const float4*>(o_part + (s * rows + row) * kPrefixD + 4 * lane);
-    l += wgt * ls;
-    acc.x += wgt * o.x;
-    acc.y += wgt * o.y;
-    acc.z += wgt * o.z;
-    acc.w += wgt * o.w;
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(O + row * kPrefixD + 4 * lane) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  Merge m;
+  m.parts<2>(o_part, ml_part, rows, row, splits);
+  m.store(O, row);
 }
 
 // A few rows per KV head (single tokens): a sequence's own keys and tree, then the merge with the
@@ -992,35 +1013,12 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
   const int lane = threadIdx.x & 31;
   for (int r = threadIdx.x >> 5; r < NG; r += kTailThreads / 32) {
     const size_t row = row0 + (size_t)(r / G) * a.Hq + r % G;
-    float M = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float pm, float pl, const float4& po) {
-      if (pm == -INFINITY && pl == 0.f) return;   // nothing was visible: its O need not have been written
-      const float mn = fmaxf(M, pm), mu = mn == -INFINITY ? 0.f : mn, w0 = exp2f(M - mu), w1 = exp2f(pm - mu);
-      M = mn;
-      sum = sum * w0 + pl * w1;
-      acc = make_float4(acc.x * w0 + po.x * w1, acc.y * w0 + po.y * w1, acc.z * w0 + po.z * w1, acc.w * w0 + po.w * w1);
-    };
-    for (int x0 = 0; x0 < a.splits_s; x0 += 4) {
-      float2 ml[4];
-      float4 po[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const bool there = x0 + x < a.splits_s;
-        const size_t at = (size_t)(there ? x0 + x : 0) * rows + row;
-        ml[x] = *reinterpret_cast<const float2*>(a.ml_part + 2 * at);
-        po[x] = *reinterpret_cast<const float4*>(a.o_part + at * D + 4 * lane);
-        if (!there) ml[x] = make_float2(-INFINITY, 0.f);
-      }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) add(ml[x].x, ml[x].y, po[x]);
-    }
+    Merge merge;
+    merge.parts<4>(a.o_part, a.ml_part, rows, row, a.splits_s);
 #pragma unroll
     for (int x = 0; x < kTailStreams; ++x)
-      add(sm_m[x][r], sm_l[x][r], *reinterpret_cast<const float4*>(&sm_o[x][r][4 * lane]));
-    const float inv = (ok && sum != 0.f) ? 1.f / sum : 0.f;
-    *reinterpret_cast<uint2*>(O + row * D + 4 * lane) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      merge.add(sm_m[x][r], sm_l[x][r], *reinterpret_cast<const float4*>(&sm_o[x][r][4 * lane]));
+    merge.store(O, row);
   }
 }
 
