@@ -23,6 +23,10 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kScan = 8;                            // refs per thread and step of a scan
 constexpr int kScanStep = kScan * kPlanThreads;
 
+// Up to this many sequences and free pages the planning CTA keeps its lists in shared memory, not
+// in the workspace (each step that reads back what another thread wrote is a round trip).
+constexpr int kSmallB = 1024, kSmallList = 2048;
+
 // Workspace: header | list A [num_pages] | list B [num_pages] | need [B] | copies [B] (source page, new page, rows)
 struct PageWs {
   int32_t* head;   // [0]: number of moves (compaction)
@@ -127,6 +131,8 @@ pages_reserve_kernel(int B, int max_pages, int num_pages, int page_rows, const i
   pdl_wait();
   pdl_trigger();
   __shared__ int sums[kScan * kPlanWarps + 1];
+  __shared__ int32_t near_need[kSmallB], near_list[kSmallList];
+  int32_t* need = B <= kSmallB ? near_need : ws.need;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // pages of sequence b's first rows, or -1 when the rows are out of range
   auto pages_of = [&](int b) {
@@ -138,15 +144,18 @@ pages_reserve_kernel(int B, int max_pages, int num_pages, int page_rows, const i
     int c = 0;
     for (int i = lane; i < np; i += 32) c += table[(size_t)b * max_pages + i] < 0;
     c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0) ws.need[b] = c;
+    if (lane == 0) need[b] = c;
   }
   __syncthreads();
-  const int total = prefix_needs(ws.need, B, sums);
+  const int total = prefix_needs(need, B, sums);
+  int32_t* list = total <= kSmallList ? near_list : ws.a;
   const int avail = scan_ids(num_pages, total, sums, [&](int id) { return refs[id] <= 0; },
-                             [&](int id, int rank) { ws.a[rank] = id; });
+                             [&](int id, int rank) {
+                               if (rank < total) list[rank] = id;
+                             });
   for (int b = warp; b < B; b += kPlanWarps) {
-    const int np = pages_of(b), at = b > 0 ? ws.need[b - 1] : 0, mine = ws.need[b] - at;
-    const bool ok = np >= 0 && (mine == 0 || ws.need[b] <= avail);
+    const int np = pages_of(b), at = b > 0 ? need[b - 1] : 0, mine = need[b] - at;
+    const bool ok = np >= 0 && (mine == 0 || need[b] <= avail);
     if (lane == 0) flags[b] = ok ? 0u : MEDUSA_FLAG_CAPACITY;
     if (!ok || mine == 0) continue;
     int given = at;
@@ -156,7 +165,7 @@ pages_reserve_kernel(int B, int max_pages, int num_pages, int page_rows, const i
       const bool empty = i < np && *e < 0;
       const unsigned votes = __ballot_sync(0xffffffffu, empty);
       if (empty) {
-        const int page = ws.a[given + __popc(votes & ((1u << lane) - 1u))];
+        const int page = list[given + __popc(votes & ((1u << lane) - 1u))];
         *e = page;
         refs[page] = 1;
       }
@@ -174,6 +183,8 @@ pages_fork_kernel(int B, int max_pages, int num_pages, int page_rows, int n, con
   pdl_wait();
   pdl_trigger();
   __shared__ int sums[kScan * kPlanWarps + 1];
+  __shared__ int32_t near_need[kSmallB], near_list[kSmallList];
+  int32_t* need = n <= kSmallB ? near_need : ws.need;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int f = warp; f < n; f += kPlanWarps) {
     const int s = src[f], d = dst[f];
@@ -196,17 +207,20 @@ pages_fork_kernel(int B, int max_pages, int num_pages, int page_rows, int n, con
     bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
       flags[f] = bad ? MEDUSA_FLAG_PAGES : 0u;
-      ws.need[f] = (!bad && len % page_rows != 0) ? 1 : 0;
+      need[f] = (!bad && len % page_rows != 0) ? 1 : 0;
     }
   }
   __syncthreads();
-  const int total = prefix_needs(ws.need, n, sums);
+  const int total = prefix_needs(need, n, sums);
+  int32_t* list = total <= kSmallList ? near_list : ws.a;
   const int avail = scan_ids(num_pages, total, sums, [&](int id) { return refs[id] <= 0; },
-                             [&](int id, int rank) { ws.a[rank] = id; });
+                             [&](int id, int rank) {
+                               if (rank < total) list[rank] = id;
+                             });
   // a source's rows are read and a destination's written: no sequence is both
   for (int f = warp; f < n; f += kPlanWarps) {
-    const int rank = ws.need[f] - 1;
-    const bool wants = ws.need[f] > (f > 0 ? ws.need[f - 1] : 0);
+    const int rank = need[f] - 1;
+    const bool wants = need[f] > (f > 0 ? need[f - 1] : 0);
     const uint32_t flag = flags[f];   // read by every lane before lane 0 may change it
     __syncwarp();
     int32_t* cp = ws.copies + 3 * f;
@@ -226,7 +240,7 @@ pages_fork_kernel(int B, int max_pages, int num_pages, int page_rows, int n, con
     }
     if (lane == 0) {
       if (wants) {
-        const int page = ws.a[rank];
+        const int page = list[rank];
         cp[0] = table[(size_t)s * max_pages + full];
         cp[1] = page;
         table[(size_t)d * max_pages + full] = page;
@@ -411,7 +425,9 @@ kv_store_paged_kernel(const uint4* __restrict__ K, const uint4* __restrict__ V, 
 int max_pages_of(const medusa_cfg& c, int page_rows) { return c.L_cap / page_rows; }
 int elt_of(const medusa_cfg& c) { return c.dtype == MEDUSA_F32 ? 4 : 2; }
 
-constexpr int kCopyGrid = 152 * 8;   // 8 CTAs of 256 threads on each of the 152 SMs
+// CTAs of a copy at most, 8 of which fit an SM at a time: with four rounds of them the SMs end
+// together (compacting 48 sequences' pages 246 us with one round, 229 with four; 31 forks 81, 72).
+constexpr int kCopyGrid = 152 * 32;
 
 }  // namespace
 
@@ -462,8 +478,12 @@ cudaError_t launch_pages_compact(const medusa_cfg& c, void* Kp, void* Vp, int nu
   if (e != cudaSuccess) return e;
   const int per16 = 16 / elt_of(c);
   const int page_vec = c.Hkv * page_rows * (c.D / per16);
-  e = launch_pdl(pages_compact_move_kernel, kCopyGrid, kCopyThreads, 0, st, static_cast<uint4*>(Kp), static_cast<uint4*>(Vp),
-                 pool_layer_elems / per16, page_vec, n_layers, table, (size_t)c.B * max_pages_of(c, page_rows), num_pages,
+  // at most half of the pages move; and every table entry is looked at
+  const size_t entries = (size_t)c.B * max_pages_of(c, page_rows), pieces = (page_vec + kCopyVec - 1) / kCopyVec;
+  const size_t most = (size_t)(num_pages / 2) * n_layers * 2 * pieces, look = (entries + kCopyThreads - 1) / kCopyThreads;
+  const size_t want = most > look ? most : look;
+  e = launch_pdl(pages_compact_move_kernel, (unsigned)(want < kCopyGrid ? want : kCopyGrid), kCopyThreads, 0, st, static_cast<uint4*>(Kp), static_cast<uint4*>(Vp),
+                 pool_layer_elems / per16, page_vec, n_layers, table, entries, num_pages,
                  static_cast<const int32_t*>(page_map), w);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();

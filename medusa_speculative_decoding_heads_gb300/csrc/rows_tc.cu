@@ -860,13 +860,14 @@ rows_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml
 // A few rows per KV head (single tokens): a sequence's own keys and tree, then the merge with the
 // parts of the shared rows, one CTA of 8 or 16 half-warps per (sequence, KV head). Bound by the K/V
 // bytes of the own rows: 16 lanes read a key's 256 bytes, each half-warp X keys at a time with the
-// next X on their way, and keep R rows of q and O in registers (8 head dims per lane). A tensor-core unit per (sequence,
-// KV head) would spend its time on barriers: 24 tokens of 40 heads behind 4096 rows 56 us, so
-// 47 us. R: the rows, N * G, rounded up to a power of two.
+// next X on their way, and keep R rows of q and O in registers (8 head dims per lane). Such a CTA
+// is a chain of a few loads, so that latency counts: 24 us for 31 MB. A tensor-core unit per
+// (sequence, KV head) would spend its time on barriers: 24 tokens of 40 heads behind 4096 rows
+// 56 us, so 44 us. R: the rows, N * G, rounded up to a power of two.
 constexpr int kTailRows = 8, kTailAhead = 1024;
 
 template <int R, int X, int kTailThreads>
-__global__ void __launch_bounds__(kTailThreads)
+__global__ void __launch_bounds__(kTailThreads, R == 1 ? 3 : 1)
 prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ Kp, const uint16_t* __restrict__ Vp,
                    const uint16_t* __restrict__ Kt, const uint16_t* __restrict__ Vt, const RowsArgs a,
                    uint16_t* __restrict__ O) {
