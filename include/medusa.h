@@ -336,11 +336,12 @@ MEDUSA_API int medusa_tree_attention_noalloc(const medusa_cfg* cfg, const void* 
  * the product with V. Rows of O that no sequence owns are left as they are.
  * cu_rows must not decrease; a sequence with cu_rows[b] < 0, cu_rows[b+1] <
  * cu_rows[b] or cu_rows[b+1] > T is skipped. Non-finite values stay within
- * their own sequence. O must not overlap Q, K or V. T = 0 enqueues nothing.
- * From cfg only B, Hq, Hkv, D and dtype are used (every prompt length is
- * allowed, whatever L_cap). Q, K, V, O 16-byte aligned; strides multiples of 16
- * bytes and at least Hq * D (Hkv * D): MEDUSA_ERR_INVALID_ARG otherwise. Needs
- * no workspace. */
+ * their own sequence (there, a value of V that is no number may reach earlier
+ * rows too). O must not overlap Q, K or V. T = 0 enqueues nothing. From cfg only
+ * B, Hq, Hkv, D and dtype are used (every prompt length is allowed, whatever
+ * L_cap), but all of it is checked. Q, K, V, O 16-byte aligned; strides multiples
+ * of 16 bytes and at least Hq * D (Hkv * D): MEDUSA_ERR_INVALID_ARG otherwise.
+ * Needs no workspace. */
 MEDUSA_API int medusa_prompt_attention(const medusa_cfg* cfg, const void* Q, const void* K, const void* V, int32_t T,
                                        int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t* cu_rows,
                                        void* O, medusa_stream_t stream);
@@ -373,10 +374,12 @@ MEDUSA_API int medusa_kv_store_paged(const medusa_cfg* cfg, const void* K, const
  * sequence is a tree of one node (cfg->tree_nodes = 1). All query rows that share
  * a KV head meet each tile of the prefix together; the rest is attended per
  * sequence; the partial results merge by their maxima and exp-sums ("최적화 2편"
- * (beengineer500), section 3.3). A row of the cache past L_b never reaches a
- * result, whatever it holds. bf16 with D = 128 only (MEDUSA_ERR_UNSUPPORTED
- * otherwise). The workspace has medusa_prefix_workspace_size() bytes (256-byte
- * aligned); each call writes all of it that it reads. */
+ * (beengineer500), section 3.3). Rows past L_b in a sequence's own pages never
+ * reach a result, whatever they hold. bf16 with D = 128 only, and at most 2^31 - 1
+ * query rows and page planes (MEDUSA_ERR_UNSUPPORTED otherwise). The workspace has
+ * medusa_prefix_workspace_size() bytes (256-byte aligned); each call writes all of
+ * it that it uses, so calls one after the other may share it and calls that may
+ * overlap may not. */
 MEDUSA_API int medusa_prefix_workspace_size(const medusa_cfg* cfg, int32_t shared_rows, size_t* bytes);
 MEDUSA_API int medusa_tree_attention_prefix(const medusa_cfg* cfg, const void* Q, const void* Kp, const void* Vp,
                                             int32_t num_pages, int32_t page_rows, const int32_t* prefix_table,
@@ -442,8 +445,9 @@ MEDUSA_API int medusa_pages_compact(const medusa_cfg* cfg, void* Kp, void* Vp, i
                                     int32_t n_layers, size_t pool_layer_elems, int32_t* block_table, int32_t* refs,
                                     int32_t* page_map, int32_t* n_live, void* workspace, medusa_stream_t stream);
 
-/* Failure detection. Every spin-wait of the tcgen05 kernels (the heads GEMVs and
- * tree attention: pipeline mbarriers, the softmax exchanges) is bounded by a
+/* Failure detection. Every spin-wait of the tcgen05 kernels (the heads GEMVs, and
+ * tree, prompt and prefix attention, which share the attention word: pipeline
+ * mbarriers, the softmax exchanges) is bounded by a
  * clock budget of about two seconds. On expiry the waiting thread ORs a code
  * naming the wait into a device word of its kernel family, leaves its loop, and
  * the kernel returns; the GPU context stays usable, but that call's outputs are
