@@ -196,6 +196,30 @@ def test_store(dtype, D, Hkv, start):
 
 
 @pytest.mark.gpu
+def test_pages_past_32_bit_offsets():
+    """Pools of more than 2^31 elements a layer: a store, a fork and a compaction at their far end."""
+    dev = gpu_ready()
+    num = 16500
+    c = Cache(3, 4, 4, dev, Hkv=8, D=128, layers=1, seed=12)
+    c.num, c.o.refs = num, [1] * (num - 6) + [0] * 6     # all but the last pages belong to others
+    c.Kp, c.Vp = (torch.zeros((1, num, 8, 128, 128), dtype=BF16, device=dev) for _ in range(2))
+    assert c.Kp.numel() > 2 ** 31
+    c.o.pools = [c.Kp.clone(), c.Vp.clone()]
+    c.set()
+    c.ws = torch.empty(mb.pages_workspace_size(c.cfg, num), dtype=torch.uint8, device=dev)
+    c.reserve([300, 0, 0])
+    k, v = (torch.randn((300, 8, 128), device=dev).to(BF16) for _ in range(2))
+    mb.kv_store_paged(c.cfg, k, v, 300, 1024, 1024, i32([0, 300, 300, 300], dev), None, c.Kp, c.Vp, num, c.P, c.table)
+    c.o.store(k, v, [0, 300, 300, 300], None)
+    c.lengths([300, 0, 0])
+    c.same("store")
+    c.fork([0], [2])
+    c.o.refs[5] = c.o.refs[16000] = 0
+    c.set()
+    c.compact()
+
+
+@pytest.mark.gpu
 def test_store_skips_what_it_may_not_write():
     """Negative and far starts, pages outside the pool, offsets past T or decreasing: nothing else changes."""
     dev = gpu_ready()

@@ -1,11 +1,12 @@
 """medusa_tree_attention_prefix: tree attention of a batch behind one shared prefix, against float64."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
-from medusa_speculative_decoding_heads_gb300 import _build, binding as mb
-from oracle import serving_oracle as SO
+from medusa_speculative_decoding_heads_gb300 import _build, binding as mb, configs
+from oracle import medusa_oracle as O, serving_oracle as SO
 
 from _helpers import gpu_ready
 from _serving import ancestor_bits, assert_within, cfg_for, i32, tolerance
@@ -51,7 +52,8 @@ class Case:
             self.Vp.transpose(1, 2)[bad] = float("nan")
         self.L, self.Hq, self.Hkv, self.branching = list(L), Hq, Hkv, branching
         self.cfg = cfg_for(self.B, Hq, Hkv, 128, BF16, self.L_cap, branching)
-        self.ws = torch.full((max(mb.prefix_workspace_size(self.cfg, shared), 256),), 255, dtype=torch.uint8, device=dev)
+        self.ws = None if dev == "cpu" else torch.full((max(mb.prefix_workspace_size(self.cfg, shared), 256),), 255,
+                                                       dtype=torch.uint8, device=dev)
 
     def call(self, O=None, stream=None, shared=None):
         O = torch.full_like(self.Q, 7.0) if O is None else O
@@ -175,6 +177,80 @@ def test_streams_graph_and_workspace():
     for _ in range(2):
         small.check(small.call(), "small call in the same workspace")
         c.check(c.call(), "large call in the same workspace")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 2), (8, 1)])
+@pytest.mark.parametrize("count", [64, 128])
+def test_pruned_trees_up_to_the_limit(count, Hq, Hkv):
+    """Trees of 64 and of 128 nodes (the most there may be), given by their rank paths."""
+    dev = gpu_ready()
+    paths = configs.pruned_paths(5, 8, count - 1)
+    branching = tuple(1 + max(p[d] for p in paths if len(p) > d) for d in range(5))
+    w = configs.scaled(configs.get("vicuna7b_b1"), branching=branching, tree_paths=paths)
+    c = Case([300, 256, 0, 700], 256, 128, Hq, Hkv, (2, 2), dev, seed=count, poison=False, L_cap=1024)
+    c.mask = torch.from_numpy(O.ancestor_mask(np.array(w.tree_nodes[0])).astype(bool))
+    c.bits = torch.from_numpy(O.mask_bits(c.mask.numpy().astype(np.uint8)).view(np.int64)).to(dev)
+    c.N, c.cfg = count, cfg_for(4, Hq, Hkv, 128, BF16, 1024, branching, tree_nodes=w.tree_nodes)
+    gen = torch.Generator(device=dev).manual_seed(count)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=dev).to(BF16)
+    c.Q, c.Kt, c.Vt = rnd(4, count, Hq, 128), rnd(4, Hkv, count, 128), rnd(4, Hkv, count, 128)
+    c.ws = torch.empty(mb.prefix_workspace_size(c.cfg, 256), dtype=torch.uint8, device=dev)
+    c.check(c.call())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("branching", [(1,), (2, 2)], ids=str)
+def test_everything_shared(branching):
+    """As many shared rows as the cache has: no sequence has rows of its own."""
+    dev = gpu_ready()
+    c = Case([0, 100, 500, 512 - (1 if branching == (1,) else 7)], 512, 128, 4, 2, branching, dev, seed=7, L_cap=512)
+    c.check(c.call())
+
+
+@pytest.mark.gpu
+def test_one_sequence_behind_a_very_long_prefix():
+    """The most key splits there are (32), and their merge."""
+    dev = gpu_ready()
+    c = Case([20000], 16384, 256, 2, 1, (1,), dev, seed=8)
+    c.check(c.call())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P", [384, 1024])
+def test_page_sizes(P):
+    dev = gpu_ready()
+    c = Case([P + 5, 1300, 640, 2000], 640, P, 8, 2, (3, 2, 2), dev, seed=P, poison=True, L_cap=3 * P if P > 900 else 6 * P)
+    c.check(c.call())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,branching", [(3, (3, 2, 2)), (20, (1,))])
+def test_pages_past_32_bit_offsets(B, branching):
+    """Pools of more than 2^31 elements, the pages in use at their far end."""
+    dev = gpu_ready()
+    c = Case([300 + 31 * b for b in range(B)], 256, 128, 16, 8, branching, dev, seed=11)
+    first = 17000 - c.num
+    far = lambda pool: torch.cat([torch.zeros((first, 8, 128, 128), dtype=BF16, device=dev), pool])
+    c.Kp, c.Vp = far(c.Kp), far(c.Vp)
+    c.prefix = [p + first for p in c.prefix]
+    c.table = [[p + first if p >= 0 else p for p in row] for row in c.table]
+    c.num = 17000
+    assert c.Kp.numel() > 2 ** 31
+    c.check(c.call())
+
+
+# ----------------------------------------------------------------------------- the oracle (no GPU)
+def test_oracle_is_the_paged_oracle():
+    """Where every sequence's own table names the shared pages, the plain paged tree attention is the same."""
+    c = Case([300, 256, 0, 411], 256, 128, 4, 2, (3, 2, 2), "cpu", seed=9, L_cap=640)
+    got, A, S = SO.prefix_attention(c.Q, c.Kp, c.Vp, 128, c.prefix, 256, c.table, c.Kt, c.Vt, c.L, c.mask, c.L_cap)
+    full = np.array([c.prefix + row[2:] for row in c.table])
+    f64 = lambda t: t.float().numpy().astype(np.float64)
+    want = O.tree_attention_paged(f64(c.Q), f64(c.Kp), f64(c.Vp), np.maximum(full, 0), 128, f64(c.Kt), f64(c.Vt), np.array(c.L),
+                                  c.mask.numpy().astype(np.uint8), 4, 2)
+    assert np.abs(got.numpy() - want).max() < 1e-12
+    assert bool((A >= got.abs() - 1e-12).all()) and bool((S >= 0).all())
 
 
 # ----------------------------------------------------------------------------- refusals (no GPU)

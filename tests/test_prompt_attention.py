@@ -202,6 +202,24 @@ def test_same_inputs_same_bits(dtype, D):
         assert torch.equal(call(q, k, v, cu), first)
 
 
+# ----------------------------------------------------------------------------- the oracle (no GPU)
+def test_oracle_is_causal_attention():
+    """Against torch's attention in float64, each sequence on its own; rows outside stay 0."""
+    gen = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn((60, h, 64), generator=gen) for h in (6, 2, 2))
+    cu = [5, 5, 25, 26, 55]
+    O, A, S = SO.prompt_attention(q, k, v, cu)
+    for a, e in zip(cu[:-1], cu[1:]):
+        if e == a:
+            continue
+        t = lambda x: x[a:e].double().transpose(0, 1)
+        want = torch.nn.functional.scaled_dot_product_attention(t(q), t(k).repeat_interleave(3, 0), t(v).repeat_interleave(3, 0),
+                                                                is_causal=True).transpose(0, 1)
+        assert (O[a:e] - want).abs().max() < 1e-12
+    assert bool((O[:5] == 0).all()) and bool((O[55:] == 0).all())
+    assert bool((A >= O.abs() - 1e-12).all()) and bool((S[5:55] > 0).all())
+
+
 # ----------------------------------------------------------------------------- refusals (no GPU)
 def status(T=8, q_stride=None, k_stride=None, v_stride=None, q=4096, k=4096, v=4096, cu=4096, o=4096, dtype=BF16, D=128,
            Hq=4, Hkv=2, **kw):
