@@ -491,7 +491,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     // One elected lane walks the schedule and issues; little but waits stands between two
     // batches of products, since whatever does is time without a product in flight (as a loop of
     // the whole warp with a vote after each wait: 1520 us for a 16384-token prompt, so: 1370).
-    // What is left: a pair of tiles takes 2700 clocks for 2048 of products. Both operands of S
+    // What is left: a pair of tiles takes 2650 clocks for 2048 of products. Both operands of S
     // come from shared memory, 8 KB per 64 clocks; with V and the arriving tiles the products
     // ask for 2048 clocks of its bandwidth as well (TMEM has no room for Q beside S and O).
     constexpr uint32_t idS = tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
@@ -681,32 +681,15 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 v[32 * c + x] = (see[c] >> x) & 1u ? v[32 * c + x] : __float_as_uint(-INFINITY);
             }
           }
-          // The first 64 weights with the maximum as it stands, while the tile's own is found;
-          // again only where it has to move (and at the first tile).
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           float corr = 1.f;
           uint32_t pk[16];
-          const bool fresh = __any_sync(0xffffffffu, m_run == -INFINITY);
-          if (!fresh) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              exp32(v + 32 * c, a.scale_log2, -m_run, pk, acc);
-              tc::tmem_st16(tS + 32 * c, pk);   // P of keys [32 c, 32 c + 32) over the first half of their scores
-            }
-          }
           const float m_tile = fmaxf(fmaxf(max32(v), max32(v + 32)), fmaxf(max32(v + 64), max32(v + 96))) * a.scale_log2;
           const bool move = m_tile > m_run + kLazy;   // also on the first visible tile (m_run = -inf): corr = 0
-          if (fresh || __any_sync(0xffffffffu, move)) {
+          if (__any_sync(0xffffffffu, move)) {
             if (move) {
               corr = tc::ex2(m_run - m_tile);
               m_run = m_tile;
-            }
-            const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
-            acc[0] = acc[1] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              exp32(v + 32 * c, a.scale_log2, neg_m, pk, acc);
-              tc::tmem_st16(tS + 32 * c, pk);
             }
             if (j > 0) {   // O += P_{j-1} V_{j-1} was issued before S_j and has landed with it
 #pragma unroll 1
@@ -718,6 +701,14 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * corr);
                 tc::tmem_st8(tO + 8 * c, o);
               }
+            }
+          }
+          {
+            const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              exp32(v + 32 * c, a.scale_log2, neg_m, pk, acc);
+              tc::tmem_st16(tS + 32 * c, pk);
             }
           }
           tc::tmem_wait_st();
