@@ -283,7 +283,8 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                const __grid_constant__ CUtensorMap tmVt, const __grid_constant__ RowsArgs a) {
   using Lay = Layout<kD>;
   constexpr int kStages = Lay::stages, kTile = Lay::tile, kHalves = Lay::halves;
-  pdl_trigger();
+  // (Behind a prefix the next kernel's blocks, started early, would crowd the SMs that are done first.)
+  if (!kPrefix) pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = sm + Lay::ring;
@@ -849,25 +850,26 @@ rows_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml
 }
 
 // A few rows per KV head (single tokens): a sequence's own keys and tree, then the merge with the
-// parts of the shared rows, one CTA of 8 or 16 half-warps per (sequence, KV head). Bound by the K/V
+// parts of the shared rows, one CTA of 8 half-warps per (sequence, KV head). Bound by the K/V
 // bytes of the own rows: 16 lanes read a key's 256 bytes, each half-warp X keys at a time with the
-// next X on their way, and keep R rows of q and O in registers (8 head dims per lane). Such a CTA
-// is a chain of a few loads, so that latency counts: 24 us for 31 MB. A tensor-core unit per
-// (sequence, KV head) would spend its time on barriers: 24 tokens of 40 heads behind 4096 rows
-// 56 us, so 44 us. R: the rows, N * G, rounded up to a power of two.
-constexpr int kTailRows = 8, kTailAhead = 1024;
+// next X on their way, and keep R rows of q and O in registers (8 head dims per lane). R: the
+// rows, N * G, rounded up to a power of two. Alone, 24 sequences of 40 heads: 10 us with 63 own
+// rows each (3 TB/s), 17 with 1 to 294, where the longest is a chain. A tensor-core unit per
+// (sequence, KV head) would spend its time on barriers: behind 4096 shared rows 56 us, so 42.
+constexpr int kTailThreads = 128, kTailStreams = kTailThreads / 16, kTailRows = 8, kTailAhead = 1024;
 
-template <int R, int X, int kTailThreads>
-__global__ void __launch_bounds__(kTailThreads, R == 1 ? 3 : 1)
+template <int R, int X>
+__global__ void __launch_bounds__(kTailThreads, R == 1 ? 6 : R == 2 ? 4 : R <= 4 ? 3 : 2)
 prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ Kp, const uint16_t* __restrict__ Vp,
                    const uint16_t* __restrict__ Kt, const uint16_t* __restrict__ Vt, const RowsArgs a,
                    uint16_t* __restrict__ O) {
-  constexpr int D = kPrefixD, kTailStreams = kTailThreads / 16;
+  constexpr int D = kPrefixD;
   __shared__ __align__(16) float sm_o[kTailStreams][R][D];
   __shared__ float sm_m[kTailStreams][R], sm_l[kTailStreams][R];
   pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv, G = a.Hq / a.Hkv, NG = a.N * G;
+  // sequences fastest: neighbouring blocks, which tend to share an SM, have different lengths
+  const int b = blockIdx.x % a.B, kvh = blockIdx.x / a.B, G = a.Hq / a.Hkv, NG = a.N * G;
   const int stream = threadIdx.x >> 4, sub = threadIdx.x & 15;
   const int Lb = a.L[b];
   const bool ok = Lb >= 0 && Lb <= a.L_cap - a.N;
@@ -1177,10 +1179,9 @@ cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const vo
   cudaError_t e;
   if (p.tail) {
     const int R = ts.N * (c.Hq / c.Hkv);
-    const auto kernel = R == 1 ? prefix_tail_kernel<1, 4, 256>
-                               : R == 2 ? prefix_tail_kernel<2, 4, 256>
-                                        : R <= 4 ? prefix_tail_kernel<4, 4, 256> : prefix_tail_kernel<8, 2, 128>;
-    e = launch_pdl(kernel, (unsigned)(c.B * c.Hkv), R <= 4 ? 256 : 128, 0, st, static_cast<const uint16_t*>(Q),
+    const auto kernel = R == 1 ? prefix_tail_kernel<1, 4>
+                               : R == 2 ? prefix_tail_kernel<2, 4> : R <= 4 ? prefix_tail_kernel<4, 4> : prefix_tail_kernel<8, 2>;
+    e = launch_pdl(kernel, (unsigned)(c.B * c.Hkv), kTailThreads, 0, st, static_cast<const uint16_t*>(Q),
                    static_cast<const uint16_t*>(Kp), static_cast<const uint16_t*>(Vp), static_cast<const uint16_t*>(Kt),
                    static_cast<const uint16_t*>(Vt), a, static_cast<uint16_t*>(O));
     note_launches(1);
