@@ -853,13 +853,14 @@ rows_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml
 // parts of the shared rows, one CTA of 8 half-warps per (sequence, KV head). Bound by the K/V
 // bytes of the own rows: 16 lanes read a key's 256 bytes, each half-warp X keys at a time with the
 // next X on their way, and keep R rows of q and O in registers (8 head dims per lane). R: the
-// rows, N * G, rounded up to a power of two. Alone, 24 sequences of 40 heads: 10 us with 63 own
-// rows each (3 TB/s), 17 with 1 to 294, where the longest is a chain. A tensor-core unit per
-// (sequence, KV head) would spend its time on barriers: behind 4096 shared rows 56 us, so 42.
+// rows, N * G, rounded up to a power of two. For R = 1 seven CTAs per SM (72 registers) hold the
+// 960 blocks of 24 sequences of 40 heads at once: alone 5.3 us with one own row each, 8.6 with 63
+// (3.7 TB/s; with six per SM 6.4 and 10.2), 18 with 1 to 294, where the longest is a chain. A tensor-core unit per
+// (sequence, KV head) would spend its time on barriers: behind 4096 shared rows 56 us, so 40.
 constexpr int kTailThreads = 128, kTailStreams = kTailThreads / 16, kTailRows = 8, kTailAhead = 1024;
 
 template <int R, int X>
-__global__ void __launch_bounds__(kTailThreads, R == 1 ? 6 : R == 2 ? 4 : R <= 4 ? 3 : 2)
+__global__ void __launch_bounds__(kTailThreads, R == 1 ? 7 : R == 2 ? 4 : R <= 4 ? 3 : 2)
 prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ Kp, const uint16_t* __restrict__ Vp,
                    const uint16_t* __restrict__ Kt, const uint16_t* __restrict__ Vt, const RowsArgs a,
                    uint16_t* __restrict__ O) {
@@ -868,8 +869,7 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
   __shared__ float sm_m[kTailStreams][R], sm_l[kTailStreams][R];
   pdl_trigger();
   pdl_wait();
-  // sequences fastest: neighbouring blocks, which tend to share an SM, have different lengths
-  const int b = blockIdx.x % a.B, kvh = blockIdx.x / a.B, G = a.Hq / a.Hkv, NG = a.N * G;
+  const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv, G = a.Hq / a.Hkv, NG = a.N * G;
   const int stream = threadIdx.x >> 4, sub = threadIdx.x & 15;
   const int Lb = a.L[b];
   const bool ok = Lb >= 0 && Lb <= a.L_cap - a.N;
