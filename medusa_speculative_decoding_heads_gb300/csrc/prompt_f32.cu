@@ -2,13 +2,16 @@
 //
 // O = softmax(q.k / sqrt(D)) v, 64 rows of one head against tiles of 64 keys, with the
 // running maximum and sum of "최적화 2편" (beengineer500), section 3.3; everything float32.
-// Bound by the float32 multiply-adds (128 per SM and clock): 4 rows keys D operations. A
-// thread owns 8 rows x 4 keys of the scores and 8 rows x D / 16 head dims of O, so that four
-// head dims (or keys) cost it 12 shared-memory words of 16 bytes, 16 wavefronts of its warp,
-// for 128 multiply-adds, issued in pairs (prompts of 700, 1, 129 and 1500 tokens, 8 heads of
-// 64: 155 us with 4 x 4 per thread, bound by shared memory; 101 us with single multiply-adds,
-// by their issue; 85 us so, 39 TFLOP/s on longer ones). Rows of Q, K and P are padded by 16
-// bytes, and a thread's rows lie 8 apart, so that no two of a warp's words meet in a bank.
+// Bound by the float32 multiply-adds (128 per SM and clock): 4 rows keys D operations. Measured
+// alone from registers they reach 68 TFLOP/s one by one and 57-61 in pairs (the registers'
+// bandwidth), but one by one they leave no issue slots for the rest, so pairs it is (prompts of
+// 700, 1, 129 and 1500 tokens, 8 heads of 64: 89 us one by one, 80 in pairs; 47 TFLOP/s on
+// longer ones). A thread owns 4 rows x 8 keys of the scores and 4 rows x D / 8 head dims of O:
+// four head dims (or keys) cost it 12 shared-memory words of 16 bytes for 128 multiply-adds. A
+// half-warp's words come in one wavefront if neighbouring lanes (or every second pair) want
+// the same one, so lane bit 0 is a row's and bit 1 a key's: 24 wavefronts per warp, 40 with
+// rows in bits 3 and 4 (86 us). Rows of Q, K and P are padded, and a thread's rows and keys
+// lie apart, so that no two words meet in a bank.
 // K_{j+1} arrives while tile j's weights and values are worked on, V_j while its scores are.
 // Groups of 128 threads (3 with D = 64, 2 with D = 128: as many as registers and shared memory
 // hold tiles for) take the unit's key tiles in turn, each with its own maximum, sum and O, and
@@ -31,7 +34,7 @@ struct Smem {
   static constexpr int groups = D == 64 ? 3 : 2;
   static constexpr int threads = groups * kGroup;
   static constexpr int ld = D + 4;            // padded row of Q and K (floats)
-  static constexpr int ldp = kTileKeys + 4;   // padded row of P
+  static constexpr int ldp = kTileKeys + 8;   // padded row of P
   static constexpr int k = kTileRows * ld;    // behind Q: K, V and P of each group
   static constexpr int v = k + kTileKeys * ld;
   static constexpr int p = v + kTileKeys * D;
@@ -67,14 +70,14 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
                   int64_t ks, int64_t vs, const int32_t* __restrict__ cu, int B, int Hq, int Hkv, float scale_log2,
                   float* __restrict__ O) {
   using S = Smem<D>;
-  constexpr int NC = D / 64;   // 4-column groups of O per thread, 64 columns apart
+  constexpr int NC = D / 32;   // 4-column groups of O per thread, 32 columns apart
   pdl_wait();
   pdl_trigger();
   extern __shared__ __align__(16) float smem[];
   __shared__ int unit_b, unit_t;
   const int group = threadIdx.x / kGroup, tid = threadIdx.x % kGroup;
   float *sq = smem, *sk = smem + S::k + group * S::per_group, *sv = sk + S::v - S::k, *sp = sk + S::p - S::k;
-  const int rg = tid >> 4, cg = tid & 15;   // rows rg + 8 i, keys cg + 16 c, head dims 4 cg + 64 n ..
+  const int rg = (tid >> 5) * 16 + ((tid & 1) | ((tid >> 3) & 2)), cg = (tid >> 1) & 7;   // rows rg + 4 i, keys cg + 8 c, head dims 4 cg + 32 n ..
   auto sync_group = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroup) : "memory"); };
 
   if (threadIdx.x < 32) {
@@ -99,10 +102,10 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
   if (group < nt) load_tile<D>(sk, S::ld, kp + (int64_t)group * kTileKeys * ks, ks, keys - group * kTileKeys, tid, kGroup);
   cp_commit();
 
-  float4 o[8][NC];
-  float m[8], l[8];
+  float4 o[4][NC];
+  float m[4], l[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
@@ -116,23 +119,29 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
     sync_group();        // ... of every thread; V and P of the tile before are no longer read
     load_tile<D>(sv, D, vp + k0 * vs, vs, keys - k0, tid, kGroup);
     cp_commit();
-    float2 s[8][4];   // (even, odd) head dims
+    float2 s[4][8];   // (even, odd) head dims
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s[i][c] = make_float2(0.f, 0.f);
-#pragma unroll 2
+      for (int c = 0; c < 8; ++c) s[i][c] = make_float2(0.f, 0.f);
+#pragma unroll 1
     for (int d = 0; d < D; d += 4) {
-      float4 w[4];
+      float4 a[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const float4*>(sk + (cg + 16 * c) * S::ld + d);
+      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (rg + 4 * i) * S::ld + d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 a = *reinterpret_cast<const float4*>(sq + (rg + 8 * i) * S::ld + d);
+      for (int h = 0; h < 8; h += 4) {
+        float4 w[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[i][c] = __ffma2_rn(make_float2(a.x, a.y), make_float2(w[c].x, w[c].y), s[i][c]);
+        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const float4*>(sk + (cg + 8 * (h + c)) * S::ld + d);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[i][c] = __ffma2_rn(make_float2(a.z, a.w), make_float2(w[c].z, w[c].w), s[i][c]);
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i][h + c] = __ffma2_rn(make_float2(a[i].x, a[i].y), make_float2(w[c].x, w[c].y), s[i][h + c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i][h + c] = __ffma2_rn(make_float2(a[i].z, a[i].w), make_float2(w[c].z, w[c].w), s[i][h + c]);
       }
     }
     sync_group();        // K_j is no longer read
@@ -140,25 +149,25 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
     if (j + S::groups < nt) load_tile<D>(sk, S::ld, kp + (int64_t)(k0 + ahead) * ks, ks, keys - k0 - ahead, tid, kGroup);
     cp_commit();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int see = r0 + rg + 8 * i - k0;   // keys 0..see of the tile are visible to the row
-      float x[4], mt = -INFINITY;
+    for (int i = 0; i < 4; ++i) {
+      const int see = r0 + rg + 4 * i - k0;   // keys 0..see of the tile are visible to the row
+      float x[8], mt = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        x[c] = cg + 16 * c <= see ? (s[i][c].x + s[i][c].y) * scale_log2 : -INFINITY;
+      for (int c = 0; c < 8; ++c) {
+        x[c] = cg + 8 * c <= see ? (s[i][c].x + s[i][c].y) * scale_log2 : -INFINITY;
         mt = fmaxf(mt, x[c]);
       }
 #pragma unroll
-      for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, w));   // the row's 16 threads
+      for (int w = 8; w > 1; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, w));   // the row's 8 threads
       const float mn = fmaxf(m[i], mt), mu = mn == -INFINITY ? 0.f : mn;
       const float corr = exp2f(m[i] - mu);
       m[i] = mn;
       float ps = 0.f;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 8; ++c) {
         const float p = exp2f(x[c] - mu);
         ps += p;
-        sp[(rg + 8 * i) * S::ldp + cg + 16 * c] = p;
+        sp[(rg + 4 * i) * S::ldp + cg + 8 * c] = p;
       }
       l[i] = l[i] * corr + ps;
 #pragma unroll
@@ -173,54 +182,55 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
     sync_group();        // ... and P_j
 #pragma unroll 2
     for (int k = 0; k < kTileKeys; k += 4) {
-      float4 w[4][NC];
+      float p[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(sp + (rg + 4 * i) * S::ldp + k);
+        p[i][0] = x.x;
+        p[i][1] = x.y;
+        p[i][2] = x.z;
+        p[i][3] = x.w;
+      }
 #pragma unroll
       for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int n = 0; n < NC; ++n) w[x][n] = *reinterpret_cast<const float4*>(sv + (k + x) * D + 64 * n + 4 * cg);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 p = *reinterpret_cast<const float4*>(sp + (rg + 8 * i) * S::ldp + k);
-#pragma unroll
         for (int n = 0; n < NC; ++n) {
-          float2 lo = make_float2(o[i][n].x, o[i][n].y), hi = make_float2(o[i][n].z, o[i][n].w);
-          const float pk[4] = {p.x, p.y, p.z, p.w};
+          const float4 w = *reinterpret_cast<const float4*>(sv + (k + x) * D + 32 * n + 4 * cg);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float2 pp = make_float2(pk[x], pk[x]);
-            lo = __ffma2_rn(pp, make_float2(w[x][n].x, w[x][n].y), lo);
-            hi = __ffma2_rn(pp, make_float2(w[x][n].z, w[x][n].w), hi);
+          for (int i = 0; i < 4; ++i) {
+            const float2 pp = make_float2(p[i][x], p[i][x]);
+            const float2 lo = __ffma2_rn(pp, make_float2(w.x, w.y), make_float2(o[i][n].x, o[i][n].y));
+            const float2 hi = __ffma2_rn(pp, make_float2(w.z, w.w), make_float2(o[i][n].z, o[i][n].w));
+            o[i][n] = make_float4(lo.x, lo.y, hi.x, hi.y);
           }
-          o[i][n] = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
-      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+    for (int w = 8; w > 1; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
   // The other groups leave their maximum, sum and O where their tiles were; group 0 merges and stores.
   if (group > 0) {
     sync_group();        // the group's last tile is no longer read
     float *so = sk, *sml = so + kTileRows * D;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = rg + 8 * i;
+    for (int i = 0; i < 4; ++i) {
+      const int r = rg + 4 * i;
       if (cg == 0) {
         sml[2 * r] = m[i];
         sml[2 * r + 1] = l[i];
       }
 #pragma unroll
-      for (int n = 0; n < NC; ++n) *reinterpret_cast<float4*>(so + r * D + 64 * n + 4 * cg) = o[i][n];
+      for (int n = 0; n < NC; ++n) *reinterpret_cast<float4*>(so + r * D + 32 * n + 4 * cg) = o[i][n];
     }
   }
   cp_wait<0>();
   __syncthreads();
   if (group > 0) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = rg + 8 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int r = rg + 4 * i;
     if (r >= rows) continue;
     // A row saw its own key at least, so its largest maximum is no -inf (unless it is no number).
     float M = m[i];
@@ -235,7 +245,7 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
       sum += so[kTileRows * D + 2 * r + 1] * w;
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
-        const float4 x = *reinterpret_cast<const float4*>(so + r * D + 64 * n + 4 * cg);
+        const float4 x = *reinterpret_cast<const float4*>(so + r * D + 32 * n + 4 * cg);
         o[i][n] = make_float4(o[i][n].x + x.x * w, o[i][n].y + x.y * w, o[i][n].z + x.z * w, o[i][n].w + x.w * w);
       }
     }
@@ -243,7 +253,7 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
     float* op = O + ((size_t)(c0 + r0 + r) * Hq + h) * D + 4 * cg;
 #pragma unroll
     for (int n = 0; n < NC; ++n)
-      *reinterpret_cast<float4*>(op + 64 * n) = make_float4(o[i][n].x * inv, o[i][n].y * inv, o[i][n].z * inv, o[i][n].w * inv);
+      *reinterpret_cast<float4*>(op + 32 * n) = make_float4(o[i][n].x * inv, o[i][n].y * inv, o[i][n].z * inv, o[i][n].w * inv);
   }
 }
 
