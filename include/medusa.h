@@ -341,7 +341,7 @@ MEDUSA_API int medusa_tree_attention_noalloc(const medusa_cfg* cfg, const void* 
  * B, Hq, Hkv, D and dtype are used (every prompt length is allowed, whatever
  * L_cap), but all of it is checked. Q, K, V, O 16-byte aligned; strides multiples
  * of 16 bytes and at least Hq * D (Hkv * D): MEDUSA_ERR_INVALID_ARG otherwise.
- * Needs no workspace. */
+ * (T / 64 + B) * Hq above 2^31 - 1: MEDUSA_ERR_UNSUPPORTED. Needs no workspace. */
 MEDUSA_API int medusa_prompt_attention(const medusa_cfg* cfg, const void* Q, const void* K, const void* V, int32_t T,
                                        int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t* cu_rows,
                                        void* O, medusa_stream_t stream);

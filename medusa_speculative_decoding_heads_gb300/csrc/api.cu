@@ -257,6 +257,8 @@ int medusa_prompt_attention(const medusa_cfg* cfg, const void* Q, const void* K,
   if (!row_stride_ok(*cfg, q_stride, cfg->Hq) || !row_stride_ok(*cfg, k_stride, cfg->Hkv) ||
       !row_stride_ok(*cfg, v_stride, cfg->Hkv))
     return MEDUSA_ERR_INVALID_ARG;
+  // units of work, one block each, are counted in 32 bits
+  if (((int64_t)T / 64 + cfg->B) * cfg->Hq > INT32_MAX) return MEDUSA_ERR_UNSUPPORTED;
   const auto launch = cfg->dtype == MEDUSA_F32 ? launch_prompt_f32 : launch_prompt_tc;
   return from_cuda(launch(*cfg, Q, K, V, T, q_stride, k_stride, v_stride, cu_rows, O, (cudaStream_t)stream));
 }

@@ -382,7 +382,7 @@ kv_store_paged_kernel(const uint4* __restrict__ K, const uint4* __restrict__ V, 
     if (row < T) {
       int lo = 0, hi = B;   // the last sequence that begins at or before the row
       while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
+        const int mid = lo + ((hi - lo) >> 1);
         if (cu[mid] <= row) lo = mid;
         else hi = mid;
       }

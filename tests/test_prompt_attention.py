@@ -221,11 +221,11 @@ def test_oracle_is_causal_attention():
 
 
 # ----------------------------------------------------------------------------- refusals (no GPU)
-def status(T=8, q_stride=None, k_stride=None, v_stride=None, q=4096, k=4096, v=4096, cu=4096, o=4096, dtype=BF16, D=128,
+def status(T=8, B=2, q_stride=None, k_stride=None, v_stride=None, q=4096, k=4096, v=4096, cu=4096, o=4096, dtype=BF16, D=128,
            Hq=4, Hkv=2, **kw):
     _build.build()
     cfg = cfg_for(2, 4, 2, D, dtype)
-    cfg.Hq, cfg.Hkv = Hq, Hkv
+    cfg.B, cfg.Hq, cfg.Hkv = B, Hq, Hkv
     ptr = lambda x: ctypes.c_void_p(x) if x else None
     return mb.load().medusa_prompt_attention(
         ctypes.byref(cfg), ptr(q), ptr(k), ptr(v), T, q_stride if q_stride is not None else Hq * D,
@@ -241,3 +241,10 @@ def status(T=8, q_stride=None, k_stride=None, v_stride=None, q=4096, k=4096, v=4
 ])
 def test_refusals(kw, want):
     assert status(**kw) == want
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_more_units_than_blocks_is_refused(dtype):
+    assert status(B=2 ** 27, Hq=32, dtype=dtype) == -2
+    assert status(B=2 ** 31 - 1, Hq=32, dtype=dtype) == -2
+    assert status(T=2 ** 31 - 1, Hq=128, dtype=dtype) == -2
