@@ -851,22 +851,32 @@ rows_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml
 
 // A few rows per KV head (single tokens): a sequence's own keys and tree, then the merge with the
 // parts of the shared rows, one CTA of 8 half-warps per (sequence, KV head). Bound by the K/V
-// bytes of the own rows: 16 lanes read a key's 256 bytes, each half-warp X keys at a time with the
-// next X on their way, and keep R rows of q and O in registers (8 head dims per lane). R: the
-// rows, N * G, rounded up to a power of two. For R = 1 seven CTAs per SM (72 registers) hold the
-// 960 blocks of 24 sequences of 40 heads at once: alone 5.3 us with one own row each, 8.6 with 63
-// (3.7 TB/s; with six per SM 6.4 and 10.2), 18 with 1 to 294, where the longest is a chain. A tensor-core unit per
-// (sequence, KV head) would spend its time on barriers: behind 4096 shared rows 56 us, so 40.
-constexpr int kTailThreads = 128, kTailStreams = kTailThreads / 16, kTailRows = 8, kTailAhead = 1024;
+// bytes of the own rows: 16 lanes read a key's 256 bytes, each half-warp X keys a step with S
+// steps on their way to shared memory, and keep R rows of q and O in registers (8 head dims per
+// lane). R: the rows, N * G, rounded up to a power of two. Alone, 24 sequences of 40 heads: 8.2 us
+// with 63 own rows each (3.8 TB/s), 22 with 256 (5.7), 11 with 1 to 294, where the longest is a
+// chain of steps; so a step of own rows that are all seen has code of its own (13.3 against 17.3 us)
+// and copies come from L2 or HBM as they may (11.1; all own rows asked for L2 first, 13.3). With
+// the next step in registers, not on its way to shared memory: 18 us. A tensor-core unit per
+// (sequence, KV head) would spend its time on barriers: behind 4096 shared rows 56 us, so 34.
+constexpr int kTailThreads = 128, kTailStreams = kTailThreads / 16, kTailRows = 8;
 
-template <int R, int X>
-__global__ void __launch_bounds__(kTailThreads, R == 1 ? 7 : R == 2 ? 4 : R <= 4 ? 3 : 2)
+__device__ __forceinline__ void cp16(uint4* dst, const uint16_t* src, bool valid) {   // (else zeros)
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::saddr(dst)), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+
+template <int R, int X, int S>
+__global__ void __launch_bounds__(kTailThreads, R == 1 ? 6 : R == 2 ? 4 : R <= 4 ? 3 : 2)
 prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ Kp, const uint16_t* __restrict__ Vp,
                    const uint16_t* __restrict__ Kt, const uint16_t* __restrict__ Vt, const RowsArgs a,
                    uint16_t* __restrict__ O) {
   constexpr int D = kPrefixD;
-  __shared__ __align__(16) float sm_o[kTailStreams][R][D];
+  // the ring: every thread's pieces of the next S steps, [step][key][K, V][thread]; then the streams' O
+  constexpr int kRing = S * X * 2 * kTailThreads * 16, kResult = kTailStreams * R * D * 4;
+  __shared__ __align__(16) uint8_t sm[kRing > kResult ? kRing : kResult];
   __shared__ float sm_m[kTailStreams][R], sm_l[kTailStreams][R];
+  uint4* ring = reinterpret_cast<uint4*>(sm) + threadIdx.x;
+  float* sm_o = reinterpret_cast<float*>(sm);
   pdl_trigger();
   pdl_wait();
   const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv, G = a.Hq / a.Hkv, NG = a.N * G;
@@ -876,18 +886,6 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
   const int own = ok ? max(0, Lb - a.shared) : 0, keys = ok ? own + a.N : 0;
   const size_t row0 = (size_t)b * a.N * a.Hq + kvh * G;   // row r: + r / G * Hq + r % G
 
-  // All of the own rows start for L2 at once (a row per thread), so that the steps below wait for
-  // L2 and not, one after the other, for DRAM.
-  for (int i = threadIdx.x; i < min(own, kTailAhead); i += kTailThreads) {
-    const int row = a.shared + i, page = a.table[(size_t)b * a.max_pages + row / a.page_rows];
-    if (page < 0 || page >= a.num_pages) continue;
-    const size_t at = (((size_t)page * a.Hkv + kvh) * a.page_rows + row % a.page_rows) * D;
-#pragma unroll
-    for (int x = 0; x < D; x += 64) {
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(Kp + at + x));
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(Vp + at + x));
-    }
-  }
   auto unpack8 = [](const uint4& x, float* f) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -897,35 +895,45 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
     }
   };
   // A step is kStep keys, X per stream; as page_rows and shared are multiples of 128, a step's own
-  // rows lie in one page, whose id is fetched two steps ahead.
+  // rows lie in one page, whose id is fetched a step before its rows are.
   constexpr int kStep = kTailStreams * X;
   static_assert(128 % kStep == 0, "a step must not cross a page");
   auto page_of = [&](int k0) { return k0 < own ? a.table[(size_t)b * a.max_pages + (a.shared + k0) / a.page_rows] : -1; };
-  uint4 kr[X], vr[X];
-  auto fetch = [&](int k0, int page) {
+  auto fetch = [&](int k0, int stage, int page) {
     const bool in_pool = page >= 0 && page < a.num_pages;
     MEDUSA_CHECK(k0 >= own || in_pool, MEDUSA_CHECK_PAGE);
-    const size_t own_at = (((size_t)(in_pool ? page : 0) * a.Hkv + kvh) * a.page_rows + (a.shared + k0) % a.page_rows) * D + 8 * sub;
+    const size_t own_at = (((size_t)(in_pool ? page : 0) * a.Hkv + kvh) * a.page_rows + (a.shared + k0) % a.page_rows + stream * X) * D + 8 * sub;
+    if (k0 + kStep <= own && in_pool) {
 #pragma unroll
-    for (int x = 0; x < X; ++x) {
-      const int i = stream * X + x, key = k0 + i;
-      const uint16_t *kp = nullptr, *vp = nullptr;
-      if (key < own) {
-        if (in_pool) {   // (outside the pool: zeros, as the tensor-core path reads)
-          kp = Kp + own_at + (size_t)i * D;
-          vp = Vp + own_at + (size_t)i * D;
-        }
-      } else if (key < keys) {
-        const size_t at = (((size_t)b * a.Hkv + kvh) * a.N + key - own) * D + 8 * sub;
-        kp = Kt + at;
-        vp = Vt + at;
+      for (int x = 0; x < X; ++x) {
+        cp16(ring + ((stage * X + x) * 2) * kTailThreads, Kp + own_at + x * D, true);
+        cp16(ring + ((stage * X + x) * 2 + 1) * kTailThreads, Vp + own_at + x * D, true);
       }
-      kr[x] = kp ? *reinterpret_cast<const uint4*>(kp) : make_uint4(0, 0, 0, 0);
-      vr[x] = kp ? *reinterpret_cast<const uint4*>(vp) : make_uint4(0, 0, 0, 0);
+    } else if (k0 < keys) {
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        const int key = k0 + stream * X + x;
+        const uint16_t *kp = Kp, *vp = Vp;
+        bool live = false;
+        if (key < own) {   // (outside the pool: zeros, as the tensor-core path reads)
+          live = in_pool;
+          kp += own_at + x * D;
+          vp += own_at + x * D;
+        } else if (key < keys) {
+          const size_t at = (((size_t)b * a.Hkv + kvh) * a.N + key - own) * D + 8 * sub;
+          live = true;
+          kp = Kt + at;
+          vp = Vt + at;
+        }
+        cp16(ring + ((stage * X + x) * 2) * kTailThreads, kp, live);
+        cp16(ring + ((stage * X + x) * 2 + 1) * kTailThreads, vp, live);
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  int page = page_of(kStep);
-  fetch(0, page_of(0));
+#pragma unroll
+  for (int i = 0; i < S; ++i) fetch(i * kStep, i, page_of(i * kStep));
+  int page = page_of(S * kStep);
   float q[R][8], o[R][8], m[R], l[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -938,15 +946,15 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
       o[r][d] = 0.f;
     }
   }
-  // (every lane of a warp takes every step: the reductions are collective)
-  for (int k0 = 0; k0 < keys; k0 += kStep) {
+  // One step; full: every key is one of the sequence's own rows and seen. (Every lane of a warp takes
+  // every step: the reductions are collective.)
+  auto step = [&](auto full_c, int k0, int st) {
+    constexpr bool full = decltype(full_c)::value;
     float s[R][X];
-    uint4 vc[X];
 #pragma unroll
     for (int x = 0; x < X; ++x) {
       float k[8];
-      unpack8(kr[x], k);
-      vc[x] = vr[x];
+      unpack8(ring[((st * X + x) * 2) * kTailThreads], k);
       const int key = k0 + stream * X + x, node = key - own;   // node >= 0: of the tree
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -955,47 +963,58 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
         for (int d = 0; d < 8; ++d) t = fmaf(q[r][d], k[d], t);
 #pragma unroll
         for (int w = 8; w > 0; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
-        bool see = key < keys && r < NG;
-        if (see && node >= 0) see = (a.bits[2 * (r / G) + (node >> 6)] >> (node & 63)) & 1ull;
+        bool see = true;
+        if (!full) {
+          see = key < keys && r < NG;
+          if (see && node >= 0) see = (a.bits[2 * (r / G) + (node >> 6)] >> (node & 63)) & 1ull;
+        }
         s[r][x] = see ? t : -INFINITY;
       }
     }
-    const int next = page;
-    page = page_of(k0 + 2 * kStep);
-    fetch(k0 + kStep, next);
     float p[R][X];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float mn = m[r];
 #pragma unroll
       for (int x = 0; x < X; ++x) mn = fmaxf(mn, s[r][x]);
-      const float mu = mn == -INFINITY ? 0.f : mn, corr = exp2f(m[r] - mu);
+      const float mu = mn == -INFINITY ? 0.f : mn, corr = tc::ex2(m[r] - mu);
       m[r] = mn;
       l[r] *= corr;
 #pragma unroll
       for (int d = 0; d < 8; ++d) o[r][d] *= corr;
 #pragma unroll
       for (int x = 0; x < X; ++x) {
-        p[r][x] = exp2f(s[r][x] - mu);
+        p[r][x] = tc::ex2(s[r][x] - mu);
         l[r] += p[r][x];
       }
     }
 #pragma unroll
     for (int x = 0; x < X; ++x) {
       float v[8];
-      unpack8(vc[x], v);
+      unpack8(ring[((st * X + x) * 2 + 1) * kTailThreads], v);
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if (s[r][x] != -INFINITY) {   // what is masked may hold anything
+        if (full || s[r][x] != -INFINITY) {   // what is masked may hold anything
 #pragma unroll
           for (int d = 0; d < 8; ++d) o[r][d] = fmaf(p[r][x], v[d], o[r][d]);
         }
     }
+  };
+  for (int k0 = 0, st = 0; k0 < keys; k0 += kStep, st = st + 1 == S ? 0 : st + 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");   // a thread reads back what it copied itself
+    if (k0 + kStep <= own) step(std::true_type{}, k0, st);
+    else step(std::false_type{}, k0, st);
+    const int next = page;
+    page = page_of(k0 + (S + 1) * kStep);
+    fetch(k0 + S * kStep, st, next);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();   // the ring is no longer read or written
 #pragma unroll
   for (int r = 0; r < R; ++r) {
 #pragma unroll
-    for (int d = 0; d < 8; ++d) sm_o[stream][r][8 * sub + d] = o[r][d];
+    for (int d = 0; d < 8; d += 4)
+      *reinterpret_cast<float4*>(sm_o + (stream * R + r) * D + 8 * sub + d) = make_float4(o[r][d], o[r][d + 1], o[r][d + 2], o[r][d + 3]);
     if (sub == 0) {
       sm_m[stream][r] = m[r];
       sm_l[stream][r] = l[r];
@@ -1011,7 +1030,7 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
     merge.parts<4>(a.o_part, a.ml_part, rows, row, a.splits_s);
 #pragma unroll
     for (int x = 0; x < kTailStreams; ++x)
-      merge.add(sm_m[x][r], sm_l[x][r], *reinterpret_cast<const float4*>(&sm_o[x][r][4 * lane]));
+      merge.add(sm_m[x][r], sm_l[x][r], *reinterpret_cast<const float4*>(sm_o + (x * R + r) * D + 4 * lane));
     merge.store(O, row);
   }
 }
@@ -1179,8 +1198,8 @@ cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const vo
   cudaError_t e;
   if (p.tail) {
     const int R = ts.N * (c.Hq / c.Hkv);
-    const auto kernel = R == 1 ? prefix_tail_kernel<1, 4>
-                               : R == 2 ? prefix_tail_kernel<2, 4> : R <= 4 ? prefix_tail_kernel<4, 4> : prefix_tail_kernel<8, 2>;
+    const auto kernel = R == 1 ? prefix_tail_kernel<1, 4, 2>
+                               : R == 2 ? prefix_tail_kernel<2, 4, 2> : R <= 4 ? prefix_tail_kernel<4, 4, 2> : prefix_tail_kernel<8, 2, 3>;
     e = launch_pdl(kernel, (unsigned)(c.B * c.Hkv), kTailThreads, 0, st, static_cast<const uint16_t*>(Q),
                    static_cast<const uint16_t*>(Kp), static_cast<const uint16_t*>(Vp), static_cast<const uint16_t*>(Kt),
                    static_cast<const uint16_t*>(Vt), a, static_cast<uint16_t*>(O));
