@@ -377,8 +377,8 @@ MEDUSA_API int medusa_kv_store_paged(const medusa_cfg* cfg, const void* K, const
  * (beengineer500), section 3.3). Rows past L_b in a sequence's own pages never
  * reach a result, whatever they hold. bf16 with D = 128 only, and at most 2^31 - 1
  * query rows and page planes (MEDUSA_ERR_UNSUPPORTED otherwise). The workspace has
- * medusa_prefix_workspace_size() bytes (256-byte aligned); each call writes all of
- * it that it uses, so calls one after the other may share it and calls that may
+ * medusa_prefix_workspace_size() bytes (256-byte aligned; NULL will do for 0); each
+ * call writes all of it that it uses, so calls one after the other may share it and calls that may
  * overlap may not. */
 MEDUSA_API int medusa_prefix_workspace_size(const medusa_cfg* cfg, int32_t shared_rows, size_t* bytes);
 MEDUSA_API int medusa_tree_attention_prefix(const medusa_cfg* cfg, const void* Q, const void* Kp, const void* Vp,

@@ -295,8 +295,8 @@ int medusa_tree_attention_prefix(const medusa_cfg* cfg, const void* Q, const voi
   if (s == MEDUSA_OK) s = check_pages(*cfg, num_pages, page_rows);
   if (s == MEDUSA_OK) s = check_prefix(*cfg, shared_rows);
   if (s != MEDUSA_OK) return s;
-  if (!Q || !Kp || !Vp || !block_table || !Kt || !Vt || !L || !anc_bits || !O || !workspace ||
-      (shared_rows > 0 && !prefix_table))
+  if (!Q || !Kp || !Vp || !block_table || !Kt || !Vt || !L || !anc_bits || !O || (shared_rows > 0 && !prefix_table) ||
+      (!workspace && prefix_workspace(*cfg, shared_rows) > 0))
     return MEDUSA_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(Kp) || !aligned16(Vp) || !aligned16(Kt) || !aligned16(Vt) || !aligned16(O))
     return MEDUSA_ERR_INVALID_ARG;

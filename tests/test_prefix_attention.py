@@ -200,6 +200,23 @@ def test_pruned_trees_up_to_the_limit(count, Hq, Hkv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shared", [0, 256])
+def test_two_nodes_a_head_for_each_query(shared):
+    """A root and its child (the root does not see the child), many sequences; lengths around each step of the keys."""
+    dev = gpu_ready()
+    L = [shared + n for n in (0, 1, 30, 31, 32, 33, 62, 63, 64, 65, 95, 96, 97, 126, 127, 128, 129, 159, 160, 200)]
+    c = Case(L, shared, 128, 8, 8, (1,), dev, seed=shared + 1, poison=True, L_cap=shared + 256)
+    c.N, c.mask = 2, torch.tensor([[True, False], [True, True]])
+    c.bits = torch.tensor([[1, 0], [3, 0]], dtype=torch.int64, device=dev)
+    gen = torch.Generator(device=dev).manual_seed(12)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=dev).to(BF16)
+    c.Q, c.Kt, c.Vt = rnd(20, 2, 8, 128) * 2, rnd(20, 8, 2, 128), rnd(20, 8, 2, 128)
+    c.cfg = cfg_for(20, 8, 8, 128, BF16, shared + 256, (1,), tree_nodes=([-1, 0], [0, 0]))
+    c.ws = torch.full((mb.prefix_workspace_size(c.cfg, shared),), 255, dtype=torch.uint8, device=dev)
+    c.check(c.call())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("branching", [(1,), (2, 2)], ids=str)
 def test_everything_shared(branching):
     """As many shared rows as the cache has: no sequence has rows of its own."""
