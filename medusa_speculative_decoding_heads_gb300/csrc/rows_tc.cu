@@ -849,24 +849,24 @@ rows_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml
   m.store(O, row);
 }
 
-// A few rows per KV head (single tokens): a sequence's own keys and tree, then the merge with the
+// One or two rows per KV head (single tokens): a sequence's own keys and tree, then the merge with the
 // parts of the shared rows, one CTA of 8 half-warps per (sequence, KV head). Bound by the K/V
 // bytes of the own rows: 16 lanes read a key's 256 bytes, each half-warp X keys a step with S
 // steps on their way to shared memory, and keep R rows of q and O in registers (8 head dims per
-// lane). R: the rows, N * G, rounded up to a power of two. Alone, 24 sequences of 40 heads: 8.2 us
-// with 63 own rows each (3.8 TB/s), 22 with 256 (5.7), 11 with 1 to 294, where the longest is a
-// chain of steps; so a step of own rows that are all seen has code of its own (13.3 against 17.3 us)
-// and copies come from L2 or HBM as they may (11.1; all own rows asked for L2 first, 13.3). With
-// the next step in registers, not on its way to shared memory: 18 us. A tensor-core unit per
-// (sequence, KV head) would spend its time on barriers: behind 4096 shared rows 56 us, so 34.
-constexpr int kTailThreads = 128, kTailStreams = kTailThreads / 16, kTailRows = 8;
+// lane; R = N * G). Alone, 24 sequences of 40 heads: 8.2 us with 63 own rows each (3.8 TB/s), 22
+// with 256 (5.7), 11 with 1 to 294, where the longest is a chain of steps; so a step of own rows
+// that are all seen has code of its own (13.3 against 17.3 us) and copies come from L2 or HBM as
+// they may (11.1; all own rows asked for L2 first, 13.3). With the next step in registers, not on
+// its way to shared memory: 18 us. A tensor-core unit per (sequence, KV head) spends its time on
+// barriers: behind 4096 shared rows 52 us, so 34.
+constexpr int kTailThreads = 128, kTailStreams = kTailThreads / 16, kTailRows = 2;
 
 __device__ __forceinline__ void cp16(uint4* dst, const uint16_t* src, bool valid) {   // (else zeros)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::saddr(dst)), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 
 template <int R, int X, int S>
-__global__ void __launch_bounds__(kTailThreads, R == 1 ? 6 : R == 2 ? 4 : R <= 4 ? 3 : 2)
+__global__ void __launch_bounds__(kTailThreads, R == 1 ? 6 : 4)
 prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ Kp, const uint16_t* __restrict__ Vp,
                    const uint16_t* __restrict__ Kt, const uint16_t* __restrict__ Vt, const RowsArgs a,
                    uint16_t* __restrict__ O) {
@@ -879,7 +879,7 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
   float* sm_o = reinterpret_cast<float*>(sm);
   pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv, G = a.Hq / a.Hkv, NG = a.N * G;
+  const int b = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv, G = a.Hq / a.Hkv;
   const int stream = threadIdx.x >> 4, sub = threadIdx.x & 15;
   const int Lb = a.L[b];
   const bool ok = Lb >= 0 && Lb <= a.L_cap - a.N;
@@ -939,10 +939,10 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
   for (int r = 0; r < R; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
-    if (r < NG) unpack8(*reinterpret_cast<const uint4*>(Q + (row0 + (size_t)(r / G) * a.Hq + r % G) * D + 8 * sub), q[r]);
+    unpack8(*reinterpret_cast<const uint4*>(Q + (row0 + (size_t)(r / G) * a.Hq + r % G) * D + 8 * sub), q[r]);
 #pragma unroll
     for (int d = 0; d < 8; ++d) {
-      q[r][d] = r < NG ? q[r][d] * a.scale_log2 : 0.f;
+      q[r][d] *= a.scale_log2;
       o[r][d] = 0.f;
     }
   }
@@ -965,7 +965,7 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
         for (int w = 8; w > 0; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
         bool see = true;
         if (!full) {
-          see = key < keys && r < NG;
+          see = key < keys;
           if (see && node >= 0) see = (a.bits[2 * (r / G) + (node >> 6)] >> (node & 63)) & 1ull;
         }
         s[r][x] = see ? t : -INFINITY;
@@ -1024,7 +1024,7 @@ prefix_tail_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ 
   // merge: a warp per row, 4 head dims per lane; the streams' results, then the shared rows' parts
   const int64_t rows = (int64_t)a.T * a.Hq;
   const int lane = threadIdx.x & 31;
-  for (int r = threadIdx.x >> 5; r < NG; r += kTailThreads / 32) {
+  for (int r = threadIdx.x >> 5; r < R; r += kTailThreads / 32) {
     const size_t row = row0 + (size_t)(r / G) * a.Hq + r % G;
     Merge merge;
     merge.parts<4>(a.o_part, a.ml_part, rows, row, a.splits_s);
@@ -1093,7 +1093,10 @@ PrefixPlan plan_prefix(const medusa_cfg& c, int shared) {
   split(HG, (int64_t)c.B * ts.N, shared, &p.units_s, &p.splits_s, &p.chunk_s, &p.dual_s);
   if (shared == 0) p.units_s = p.splits_s = 0;
   const int own = c.L_cap - ts.N - shared;
-  // a few rows per KV head, and enough (sequence, KV head) pairs to keep every SM reading
+  // One or two rows per KV head, and enough (sequence, KV head) pairs to keep every SM reading: 192
+  // pairs of one row with 63, 256 and 1024 own rows each behind 4096: 15.7, 19, 37 us so and 20.9,
+  // 21.5, 35 on the tensor cores; of four rows 20, 27, 53 and 23, 24, 39; of eight 28 and 22, 41 and
+  // 23. 64 pairs of one row 14.7, 17.6, 28 and 15.5, 14.6, 20.
   p.tail = ts.N * (c.Hq / c.Hkv) <= kTailRows && (int64_t)c.B * c.Hkv >= kSms;
   if (!p.tail) split((int64_t)c.B * HG, ts.N, own > 0 ? own : 0, &p.units_u, &p.splits_u, &p.chunk_u, &p.dual_u);
   p.parts = p.splits_s + p.splits_u;
@@ -1197,9 +1200,7 @@ cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const vo
   }
   cudaError_t e;
   if (p.tail) {
-    const int R = ts.N * (c.Hq / c.Hkv);
-    const auto kernel = R == 1 ? prefix_tail_kernel<1, 4, 2>
-                               : R == 2 ? prefix_tail_kernel<2, 4, 2> : R <= 4 ? prefix_tail_kernel<4, 4, 2> : prefix_tail_kernel<8, 2, 3>;
+    const auto kernel = ts.N * (c.Hq / c.Hkv) == 1 ? prefix_tail_kernel<1, 4, 2> : prefix_tail_kernel<2, 4, 2>;
     e = launch_pdl(kernel, (unsigned)(c.B * c.Hkv), kTailThreads, 0, st, static_cast<const uint16_t*>(Q),
                    static_cast<const uint16_t*>(Kp), static_cast<const uint16_t*>(Vp), static_cast<const uint16_t*>(Kt),
                    static_cast<const uint16_t*>(Vt), a, static_cast<uint16_t*>(O));
