@@ -148,6 +148,21 @@ def test_out_of_pages():
 
 
 @pytest.mark.gpu
+def test_many_sequences():
+    """More sequences, forks and free pages than the planning kernels' lists in shared memory hold."""
+    c = Cache(2600, 2, 5000, gpu_ready(), Hkv=1, D=64, layers=1, seed=6)
+    rows = [(37 * b) % 257 if b < 1100 else 0 for b in range(2600)]
+    c.reserve(rows)
+    c.lengths(rows)
+    dst = list(range(1100, 2600))
+    c.fork([(7 * i) % 1100 for i in range(1500)], dst)
+    c.reserve([256] * 2600)                # more than there are: in order, until the free pages end
+    c.free(list(range(0, 2600, 2)) + [4, 4])
+    c.compact()
+    c.reserve([200] * 2600)
+
+
+@pytest.mark.gpu
 def test_compact_many_pages():
     """More pages than one step of the scan takes, and no page in use or every page in use."""
     dev = gpu_ready()

@@ -149,6 +149,45 @@ def test_page_ids_outside_the_pool(branching):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq", [8, 16])
+def test_page_ids_outside_the_pool_of_many_sequences(Hq):
+    """The same for single tokens of enough sequences to fill the GPU."""
+    dev = gpu_ready()
+    c = Case([256 + 13 * b for b in range(24)], 256, 128, Hq, 8, (1,), dev, seed=14)
+    c.table[3][2], c.table[20][2], c.table[20][3] = -1, c.num, 2 ** 31 - 1
+    O = c.call()
+    c.table[3] = c.table[20] = c.table[23]   # these two are not compared
+    for rows in (slice(0, 3), slice(4, 20), slice(21, 24)):
+        c.check(O, rows=rows)
+
+
+@pytest.mark.gpu
+def test_single_tokens_streams_and_graph():
+    """Two calls at once with workspaces of their own; a captured call replayed with other lengths."""
+    dev = gpu_ready()
+    cs = [Case([256 + 17 * b for b in range(24)], 256, 128, 8, 8, (1,), dev, seed=s) for s in (15, 16)]
+    want = [c.call() for c in cs]
+    outs, streams = [torch.full_like(w, 7.0) for w in want], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for c, o, st in zip(cs, outs, streams):
+            c.call(o, st)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    c, O = cs[0], torch.full_like(want[0], 7.0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.call(O)
+        c.call(O)
+    c.L = [0, 100] + [256 + 11 * b for b in range(22)]
+    c.dL.copy_(i32(c.L, dev))
+    for _ in range(3):
+        g.replay()
+    c.check(O, "replayed")
+
+
+@pytest.mark.gpu
 def test_streams_graph_and_workspace():
     """Two calls at once with workspaces of their own; a captured call replayed with other lengths;
     two calls of different sizes that take turns with one workspace."""
