@@ -27,7 +27,7 @@
 namespace medusa {
 namespace {
 
-constexpr int kTileRows = 64, kTileKeys = 64, kGroup = 128;
+constexpr int kTileShift = 6, kTileRows = 1 << kTileShift, kTileKeys = 64, kGroup = 128;
 
 template <int D>
 struct Smem {
@@ -82,7 +82,7 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
 
   if (threadIdx.x < 32) {
     PromptWalk walk;
-    walk.begin(cu, B, T, kTileRows);
+    walk.begin(cu, B, T, kTileShift);
     const int b = walk.find((int)(blockIdx.x / Hq));
     if (threadIdx.x == 0) {
       unit_b = b;

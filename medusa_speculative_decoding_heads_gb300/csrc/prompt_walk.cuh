@@ -7,39 +7,44 @@
 
 namespace medusa {
 
-// A sequence is cut into tiles of `per` rows; units are (tile number, sequence), by tile
+// A sequence is cut into tiles of 2^shift rows; units are (tile number, sequence), by tile
 // number from the last one down, then by sequence, so that the longest units start first and
 // the shortest fill the end. A whole warp calls every function; units asked for in ascending
-// order cost little. Sequences whose bounds leave [0, T] or decrease have no tiles.
+// order cost little. Sequences whose bounds leave [0, T] or decrease have no tiles. Each lane
+// keeps the tiles of one of the first 32 sequences (a short call is a chain of such latencies).
 struct PromptWalk {
   const int32_t* cu;
-  int B, T, per;
+  int B, T, shift;
+  int mine;               // tiles of sequence `lane`
   int t, before, count;   // `count` units have tile number t; `before` come ahead of them
 
+  __device__ __forceinline__ int lane() const { return threadIdx.x & 31; }
   __device__ __forceinline__ int tiles(int b) const {
     if (b >= B) return 0;
     const int c0 = cu[b], c1 = cu[b + 1];
-    return (c0 >= 0 && c1 >= c0 && c1 <= T) ? (int)(((int64_t)(c1 - c0) + per - 1) / per) : 0;
+    return (c0 >= 0 && c1 >= c0 && c1 <= T) ? (int)(((unsigned)(c1 - c0) + (1u << shift) - 1) >> shift) : 0;
   }
   __device__ __forceinline__ int above() const {   // sequences with more than t tiles
-    int c = 0;
-    for (int b = threadIdx.x & 31; b < B; b += 32) c += tiles(b) > t;
+    if (B <= 32) return __popc(__ballot_sync(0xffffffffu, mine > t));
+    int c = mine > t;
+    for (int b = 32 + lane(); b < B; b += 32) c += tiles(b) > t;
     return __reduce_add_sync(0xffffffffu, c);
   }
-  __device__ void begin(const int32_t* cu_, int B_, int T_, int per_) {
+  __device__ void begin(const int32_t* cu_, int B_, int T_, int shift_) {
     cu = cu_;
     B = B_;
     T = T_;
-    per = per_;
-    int most = 0;
-    for (int b = threadIdx.x & 31; b < B; b += 32) most = max(most, tiles(b));
+    shift = shift_;
+    mine = tiles(lane());
+    int most = mine;
+    for (int b = 32 + lane(); b < B; b += 32) most = max(most, tiles(b));
     t = __reduce_max_sync(0xffffffffu, most) - 1;
     before = 0;
     count = t >= 0 ? above() : 0;
   }
   // Sequence of unit u (t: its tile number), or -1 past the last unit.
   __device__ int find(int u) {
-    if (u < before) begin(cu, B, T, per);
+    if (u < before) begin(cu, B, T, shift);
     while (t >= 0 && u >= before + count) {
       before += count;
       --t;
@@ -48,9 +53,12 @@ struct PromptWalk {
     if (t < 0) return -1;
     int rank = u - before;
     for (int b0 = 0; b0 < B; b0 += 32) {
-      const unsigned votes = __ballot_sync(0xffffffffu, tiles(b0 + (threadIdx.x & 31)) > t);
+      const unsigned votes = __ballot_sync(0xffffffffu, (b0 == 0 ? mine : tiles(b0 + lane())) > t);
       const int c = __popc(votes);
-      if (rank < c) return b0 + (int)__fns(votes, 0, rank + 1);
+      if (rank < c) {   // the rank-th of the votes
+        const bool it = ((votes >> lane()) & 1u) && __popc(votes & ((1u << lane()) - 1u)) == rank;
+        return b0 + __ffs(__ballot_sync(0xffffffffu, it)) - 1;
+      }
       rank -= c;
     }
     return -1;

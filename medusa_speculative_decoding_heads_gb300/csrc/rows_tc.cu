@@ -221,13 +221,13 @@ struct Piece {
 __device__ __forceinline__ Piece decode_prompt(const RowsArgs& a, PromptWalk& walk, int u, int t) {
   Piece w = {};
   const int npos = kRows >> a.gp_shift, HG = a.Hq >> a.gp_shift;
-  const int b = walk.find(u / HG);
+  const int x = u / HG, b = walk.find(x);
   if (b < 0) return w;
   const int c0 = a.cu[b], len = a.cu[b + 1] - c0, i = (2 * walk.t + t) * npos;
   w.kind = kPrompt;
   w.pos0 = c0 + i;
   w.left = len - i;
-  w.h0 = (u % HG) << a.gp_shift;
+  w.h0 = (u - x * HG) << a.gp_shift;
   w.kvh = w.h0 / (a.Hq / a.Hkv);
   w.base = c0;
   w.kend = len;
@@ -340,7 +340,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     // Block indices are units in order. The CTA begins with its own and then takes over blocks
     // that have not started, so that the SMs run out of work together.
     PromptWalk walk;
-    if (!kPrefix) walk.begin(a.cu, a.B, a.T, 2 * npos);
+    if (!kPrefix) walk.begin(a.cu, a.B, a.T, 8 - a.gp_shift);
     int u = (int)blockIdx.x, asked = 0, i = 0;   // i: units handed out
     bool ok = true;
     while (ok && u >= 0) {
