@@ -5,8 +5,8 @@
 // Bound by the float32 multiply-adds (128 per SM and clock): 4 rows keys D operations. Measured
 // alone from registers they reach 68 TFLOP/s one by one and 57-61 in pairs (the registers'
 // bandwidth), but one by one they leave no issue slots for the rest, so pairs it is (prompts of
-// 700, 1, 129 and 1500 tokens, 8 heads of 64: 89 us one by one, 80 in pairs; 47 TFLOP/s on
-// longer ones). A thread owns 4 rows x 8 keys of the scores and 4 rows x D / 8 head dims of O:
+// 700, 1, 129 and 1500 tokens, 8 heads of 64: 89 us one by one, 80 in pairs, now 76; 50
+// TFLOP/s on longer ones). A thread owns 4 rows x 8 keys of the scores and 4 rows x D / 8 head dims of O:
 // four head dims (or keys) cost it 12 shared-memory words of 16 bytes for 128 multiply-adds. A
 // half-warp's words come in one wavefront if neighbouring lanes (or every second pair) want
 // the same one, so lane bit 0 is a row's and bit 1 a key's: 24 wavefronts per warp, 40 with
