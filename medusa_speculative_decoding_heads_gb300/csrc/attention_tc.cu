@@ -533,7 +533,8 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       tc::mbar_arrive(&xbar);
       float l_tile = 0.f;
       const bool spec = m_run != -INFINITY && bf16_value(mine) <= m_run + kLazy;
-      if (__all_sync(0xffffffffu, spec)) {
+      const bool spec_all = __all_sync(0xffffffffu, spec);
+      if (spec_all) {
         if (row_ok) l_tile = exp32(v, scale_log2, -m_run, pk);
         else {
 #pragma unroll
@@ -554,7 +555,8 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
                                  fmaxf(__uint_as_float(xm[2]), __uint_as_float(xm[3])));
       float corr = 1.f;
       const bool move = m_tile > m_run + kLazy;   // also on the first visible tile (m_run = -inf)
-      if (__any_sync(0xffffffffu, move || !__all_sync(0xffffffffu, spec))) {
+      // (Two votes, each taken by the whole warp: lanes of a warp differ in `move`.)
+      if (__any_sync(0xffffffffu, move) || !spec_all) {
         if (move) {
           corr = tc::ex2(m_run - m_tile);
           m_run = m_tile;
@@ -595,6 +597,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     xl[q * kRows + row] = l_run;
     tc::mbar_arrive(&xbar);
     tc::mbar_wait(&xbar, ntiles & 1, err, 512);
+    __syncwarp();
     const float l_tot = (xl[row] + xl[kRows + row]) + (xl[2 * kRows + row] + xl[3 * kRows + row]);
     uint32_t ov[32];
     if (have) {   // warp-uniform: the TMEM load is a collective of the warp
@@ -743,6 +746,7 @@ tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
     }
     tc::mbar_arrive(&xbar2);
     const bool summed = tc::mbar_wait(&xbar2, nx & 1, err, 65536);
+    __syncwarp();
     uint32_t ov[kXMax];
     if (have) {   // warp-uniform: the TMEM load is a collective of the warp
       tc::tmem_ld8(tmem + kColO2 + xl_base, ov);
