@@ -60,6 +60,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSms = 152;
+constexpr int kLeastKeys = 256;   // of a key range that is one of several: two tiles
 constexpr int kAhead = 8;   // steps (K and V tiles) of a unit still to be loaded when the next unit is fetched
 // The running maximum moves (and O is rescaled) only when a tile's maximum exceeds it by more
 // than this many binary orders of magnitude: weights stay below 2^8, far inside bf16 and f32.
@@ -78,7 +79,7 @@ struct RowsArgs {
   int Hq, Hkv, gp_shift;   // log2 of Gp
   int L_cap, page_rows, max_pages, num_pages, shared;
   int units_s, splits_s, chunk_s, dual_s;   // units, key ranges and their length of the shared rows; 1: dual units
-  int units_u, splits_u, chunk_u, dual_u;   // the same of the sequences' own rows
+  int units_u, splits_u, dual_u;            // the same of the sequences' own rows (a length for each sequence)
   float scale_log2;
   uint16_t* O;             // prompts
   float* o_part;           // prefix: [split][row][D], row = position * Hq + head
@@ -267,8 +268,12 @@ __device__ __forceinline__ Piece decode_prefix(const RowsArgs& a, int u, int t) 
   } else {
     const int Lb = a.L[b];
     const bool ok = Lb >= 0 && Lb <= a.L_cap - a.N;
-    w.k0 = a.shared + split * a.chunk_u;
-    w.kend = ok ? min(Lb, w.k0 + a.chunk_u) : 0;
+    // The ranges divide the rows that the sequence has, not those that it may come to have: four
+    // tokens of 32 heads with 300 to 2800 own rows in a cache of 32768: 63 us by capacity, 30 so.
+    const int own = ok ? max(0, Lb - a.shared) : 0;
+    const int chunk = max(kLeastKeys, ((own + a.splits_u - 1) / a.splits_u + kKeys - 1) & ~(kKeys - 1));
+    w.k0 = a.shared + split * chunk;
+    w.kend = ok ? min(Lb, w.k0 + chunk) : 0;
     tree = ok && split == a.splits_u - 1;
   }
   w.n = w.kend > w.k0 ? (w.kend - w.k0 + kKeys - 1) / kKeys : 0;
@@ -1070,7 +1075,7 @@ int gp_shift_of(int G) {
 // tile go two pieces to a unit.
 struct PrefixPlan {
   int gp_shift, parts, tail;
-  int units_s, splits_s, chunk_s, dual_s, units_u, splits_u, chunk_u, dual_u;
+  int units_s, splits_s, chunk_s, dual_s, units_u, splits_u, dual_u;
   size_t ml_part, total;
 };
 PrefixPlan plan_prefix(const medusa_cfg& c, int shared) {
@@ -1081,7 +1086,7 @@ PrefixPlan plan_prefix(const medusa_cfg& c, int shared) {
   auto split = [&](int64_t groups, int64_t positions, int64_t keys, int* units, int* splits, int* chunk, int* dual) {
     *dual = positions <= npos;
     const int64_t tiles = groups * ((positions + 2 * npos - 1) / (2 * npos));   // units of one key range; pieces, if dual
-    int64_t want = (*dual ? 2 : 1) * kSms / tiles, most = (keys + 255) / 256;   // at least two key tiles each
+    int64_t want = (*dual ? 2 : 1) * kSms / tiles, most = (keys + kLeastKeys - 1) / kLeastKeys;
     if (want > most) want = most;
     if (want > 32) want = 32;
     if (want < 1) want = 1;
@@ -1098,7 +1103,8 @@ PrefixPlan plan_prefix(const medusa_cfg& c, int shared) {
   // 21.5, 35 on the tensor cores; of four rows 20, 27, 53 and 23, 24, 39; of eight 28 and 22, 41 and
   // 23. 64 pairs of one row 14.7, 17.6, 28 and 15.5, 14.6, 20.
   p.tail = ts.N * (c.Hq / c.Hkv) <= kTailRows && (int64_t)c.B * c.Hkv >= kSms;
-  if (!p.tail) split((int64_t)c.B * HG, ts.N, own > 0 ? own : 0, &p.units_u, &p.splits_u, &p.chunk_u, &p.dual_u);
+  int most_own;   // (a sequence's own rows are divided where its length is known)
+  if (!p.tail) split((int64_t)c.B * HG, ts.N, own > 0 ? own : 0, &p.units_u, &p.splits_u, &most_own, &p.dual_u);
   p.parts = p.splits_s + p.splits_u;
   const size_t rows = (size_t)c.B * ts.N * c.Hq;
   p.ml_part = align_up(p.parts * rows * kPrefixD * 4, 256);
@@ -1180,7 +1186,6 @@ cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const vo
   a.dual_s = p.dual_s;
   a.units_u = p.units_u;
   a.splits_u = p.splits_u;
-  a.chunk_u = p.chunk_u;
   a.dual_u = p.dual_u;
   a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)kPrefixD));
   a.o_part = static_cast<float*>(ws);
