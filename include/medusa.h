@@ -334,9 +334,9 @@ MEDUSA_API int medusa_tree_attention_noalloc(const medusa_cfg* cfg, const void* 
  *                              h / (Hq / Hkv)
  * Softmax and accumulation in float32; bf16 weights are rounded to bf16 before
  * the product with V. Rows of O that no sequence owns are left as they are.
- * cu_rows must not decrease; a sequence with cu_rows[b] < 0, cu_rows[b+1] <
- * cu_rows[b] or cu_rows[b+1] > T is skipped. Non-finite values stay within
- * their own sequence (there, a value of V that is no number may reach earlier
+ * cu_rows must not decrease: a sequence with cu_rows[b+1] < cu_rows[b] and all
+ * behind it are skipped. A sequence with cu_rows[b] < 0 or cu_rows[b+1] > T is
+ * skipped, too. Non-finite values stay within their own sequence (there, a value of V that is no number may reach earlier
  * rows too). O must not overlap Q, K or V. T = 0 enqueues nothing. From cfg only
  * B, Hq, Hkv, D and dtype are used (every prompt length is allowed, whatever
  * L_cap), but all of it is checked. Q, K, V, O 16-byte aligned; strides multiples
@@ -347,7 +347,8 @@ MEDUSA_API int medusa_prompt_attention(const medusa_cfg* cfg, const void* Q, con
                                        void* O, medusa_stream_t stream);
 
 /* A prompt's keys and values (one layer's) into the pages of a cache.
- *   K, V, T, k_stride, v_stride, cu_rows   as for medusa_prompt_attention
+ *   K, V, T, k_stride, v_stride, cu_rows   as for medusa_prompt_attention (where
+ *                              cu_rows decreases, which rows are written is not defined)
  *   start [B] int32            logical row that sequence b's row 0 becomes; NULL: 0
  *   Kp, Vp, num_pages, page_rows, block_table   as for medusa_tree_attention_paged
  *                              (any dtype and D)

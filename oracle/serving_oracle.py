@@ -37,12 +37,15 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, visible: torch.Ten
 
 
 def prompt_attention(Q, K, V, cu: Sequence[int]):
-    """Causal attention of packed sequences: (O, A, S) as ``attend``, [T][Hq][D] and [T][Hq]."""
+    """Causal attention of packed sequences, up to the first decrease of cu: (O, A, S) as ``attend``, [T][Hq][D] and
+    [T][Hq]."""
     T, Hq, D = Q.shape
     O = torch.zeros((T, Hq, D), dtype=torch.float64, device=Q.device)
     A, S = torch.zeros_like(O), torch.zeros((T, Hq), dtype=torch.float64, device=Q.device)
     for a, e in zip(cu[:-1], cu[1:]):
-        if a < 0 or e <= a or e > T:
+        if e < a:
+            break
+        if a < 0 or e == a or e > T:
             continue
         i = torch.arange(e - a, device=Q.device)
         see = i[None, :] <= i[:, None]
