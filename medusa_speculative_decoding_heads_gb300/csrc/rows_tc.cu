@@ -749,7 +749,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       const size_t orow = (size_t)pos * a.Hq + head, orow0 = (size_t)(pos - quad) * a.Hq + head;
       const int rows_here = left - (rpos - quad);   // rows of the four that exist, if positive
       if (!kPrefix) {
-        const float inv = l_run > 0.f ? 1.f / l_run : l_run;   // (a NaN sum stays NaN)
+        const float inv = 1.f / l_run;   // (0 where every visible score is -inf: 0 times inf, no number, as in float32)
 #pragma unroll 1
         for (int c = 0; c < kD / 32; ++c) {
           uint32_t o[32], pk[16];
