@@ -658,8 +658,9 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           const int Lb = a.L[b];
           limit = (Lb >= 0 && Lb <= a.L_cap - a.N) ? min(Lb, kend) : 0;
         } else if (tree_tile >= 0) {
-          word0 = a.bits[2 * (pos - b * a.N)];
-          word1 = a.bits[2 * (pos - b * a.N) + 1];
+          // (bits past the last node name no key)
+          word0 = a.bits[2 * (pos - b * a.N)] & (~0ull >> (a.N < 64 ? 64 - a.N : 0));
+          word1 = a.N > 64 ? a.bits[2 * (pos - b * a.N) + 1] & (~0ull >> (128 - a.N)) : 0;
         }
       }
       const bool busy = __any_sync(0xffffffffu, row_ok);   // a warp without rows only keeps the pace
