@@ -375,8 +375,11 @@ MEDUSA_API int medusa_kv_store_paged(const medusa_cfg* cfg, const void* K, const
  * sequence is a tree of one node (cfg->tree_nodes = 1). All query rows that share
  * a KV head meet each tile of the prefix together; the rest is attended per
  * sequence; the partial results merge by their maxima and exp-sums ("최적화 2편"
- * (beengineer500), section 3.3). Rows past L_b in a sequence's own pages never
- * reach a result, whatever they hold. bf16 with D = 128 only, and at most 2^31 - 1
+ * (beengineer500), section 3.3). Rows past L_b in a sequence's own pages, and
+ * shared rows past the longest length, never reach a result, whatever they hold.
+ * A key that a row does not see never reaches it. (A value that is no number may:
+ * from a shared row that another sequence has, or from a staged row of the same
+ * sequence. Its weight is 0, the product is not.) bf16 with D = 128 only, and at most 2^31 - 1
  * query rows and page planes (MEDUSA_ERR_UNSUPPORTED otherwise). The workspace has
  * medusa_prefix_workspace_size() bytes (256-byte aligned; NULL will do for 0); each
  * call writes all of it that it uses, so calls one after the other may share it and calls that may

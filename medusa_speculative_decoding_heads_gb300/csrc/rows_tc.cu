@@ -21,7 +21,7 @@
 //                   while the other tile's softmax does. MMAs of one issuing thread run in
 //                   order: S_t(j + 1), which overwrites P_t(j), follows O_t += P_t(j) V_j.
 //   warp 9          TMA: Q tiles, then K and V tiles of 128 keys alternating through one
-//                   ring of 160 KB. V rows past the last key that may be read are zeroed in
+//                   ring of 160 KB. V rows past the last key that any row sees are zeroed in
 //                   shared memory (0 x NaN must not reach a result).
 //   warp 10         the schedule: a unit per block of the grid, longest first; this warp takes over
 //                   blocks that have not started (cluster launch control) and decodes the next
@@ -402,6 +402,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     Unit w;
     int it = 0, nq[2] = {0, 0}, fixes = 0;   // ring position, Q tiles loaded, tails zeroed
     int page_reg[2] = {-1, -1};
+    int seen = -1;   // prefix: shared rows that any sequence sees (once it is known: rows past it may hold anything)
     bool ok = true;
     for (int i = 0; ok && next_unit(i, w); ++i) {
       const int nt = max(w.n[0], w.n[1]), tiles = w.dual ? 2 : 1;
@@ -462,7 +463,16 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           }
           const CUtensorMap* m = tree ? (isv ? &tmVt : &tmKt) : (isv ? &tmV : &tmK);
           uint8_t* dst = ring + st * kTile;
-          const int live = tree ? kKeys : min(kKeys, kend - key0);   // (rows past the tree's nodes arrive as zeros)
+          if (kPrefix && isv && seen < 0 && w.kind == kShared) {   // (K and Q are on their way)
+            seen = 0;
+            for (int b = lane; b < a.B; b += 32) {
+              const int Lb = a.L[b];
+              if (Lb <= a.L_cap - a.N) seen = max(seen, Lb);
+            }
+            seen = __reduce_max_sync(0xffffffffu, seen);
+          }
+          const int last = kPrefix && w.kind == kShared ? min(kend, seen) : kend;
+          const int live = tree ? kKeys : max(0, min(kKeys, last - key0));   // (rows past the tree's nodes arrive as zeros)
           const bool fix = isv && live < kKeys;
           uint64_t* bar = fix ? &tail : &kv_full[st];
           if (lane == 0) {
