@@ -27,6 +27,11 @@
 namespace medusa {
 namespace {
 
+// Batches of more prompts than this look for each unit's sequence from where the CTA's last one was
+// (4 CTAs per SM, one at a time): 512 of 1 to 60 rows 227 us with a CTA per unit, 189 so, 4096 of
+// them 3865 and 1541 (two CTAs per SM 185 and 1493); 128 of them and one of 4000 rows 403 and 399
+// (409), but 64 with one of 4000 373 and 385.
+constexpr int kManyPrompts = 64, kManyGrid = 4 * 152;
 constexpr int kTileShift = 6, kTileRows = 1 << kTileShift, kTileKeys = 64, kGroup = 128;
 
 template <int D>
@@ -64,35 +69,19 @@ __device__ __forceinline__ void load_tile(float* dst, int ld, const float* src, 
   }
 }
 
+// Rows r0 to r0 + 63 of sequence b in head h, by the whole CTA.
 template <int D>
-__global__ void __launch_bounds__(Smem<D>::threads, 1)
-prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V, int T, int64_t qs,
-                  int64_t ks, int64_t vs, const int32_t* __restrict__ cu, int B, int Hq, int Hkv, float scale_log2,
-                  float* __restrict__ O) {
+__device__ __forceinline__ void prompt_unit(float* smem, const float* __restrict__ Q, const float* __restrict__ K,
+                                            const float* __restrict__ V, int64_t qs, int64_t ks, int64_t vs,
+                                            const int32_t* __restrict__ cu, int Hq, int Hkv, float scale_log2,
+                                            float* __restrict__ O, int b, int r0, int h) {
   using S = Smem<D>;
   constexpr int NC = D / 32;   // 4-column groups of O per thread, 32 columns apart
-  pdl_wait();
-  pdl_trigger();
-  extern __shared__ __align__(16) float smem[];
-  __shared__ int unit_b, unit_t;
   const int group = threadIdx.x / kGroup, tid = threadIdx.x % kGroup;
   float *sq = smem, *sk = smem + S::k + group * S::per_group, *sv = sk + S::v - S::k, *sp = sk + S::p - S::k;
   const int rg = (tid >> 5) * 16 + ((tid & 1) | ((tid >> 3) & 2)), cg = (tid >> 1) & 7;   // rows rg + 4 i, keys cg + 8 c, head dims 4 cg + 32 n ..
   auto sync_group = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroup) : "memory"); };
-
-  if (threadIdx.x < 32) {
-    PromptWalk walk;
-    walk.begin(cu, B, T, kTileShift);
-    const int b = walk.find((int)(blockIdx.x / Hq));
-    if (threadIdx.x == 0) {
-      unit_b = b;
-      unit_t = walk.t;
-    }
-  }
-  __syncthreads();
-  const int b = unit_b, r0 = unit_t * kTileRows;
-  if (b < 0) return;   // (the grid may hold more blocks than there are units)
-  const int h = (int)(blockIdx.x % Hq), kvh = h / (Hq / Hkv);
+  const int kvh = h / (Hq / Hkv);
   const int64_t c0 = cu[b];
   const int len = cu[b + 1] - (int)c0, rows = min(kTileRows, len - r0), keys = r0 + rows;
   const int nt = (keys + kTileKeys - 1) / kTileKeys;
@@ -257,16 +246,51 @@ prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, cons
   }
 }
 
+// A CTA per unit; kMany: it takes unit blockIdx.x and every gridDim.x-th behind it, and keeps its
+// place among them.
+template <int D, bool kMany>
+__global__ void __launch_bounds__(Smem<D>::threads, 1)
+prompt_f32_kernel(const float* __restrict__ Q, const float* __restrict__ K, const float* __restrict__ V, int T, int64_t qs,
+                  int64_t ks, int64_t vs, const int32_t* __restrict__ cu, int B, int Hq, int Hkv, float scale_log2,
+                  unsigned units, float* __restrict__ O) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ __align__(16) float smem[];
+  __shared__ int unit_b, unit_t;
+  __shared__ PromptWalk place;
+  for (unsigned u = blockIdx.x;; u += gridDim.x) {
+    if (threadIdx.x < 32) {
+      PromptWalk walk;
+      if (!kMany || u == blockIdx.x) walk.begin(cu, B, T, kTileShift);
+      else walk = place;
+      const int b = walk.find((int)(u / Hq));
+      __syncwarp();
+      if (threadIdx.x == 0) {
+        unit_b = b;
+        unit_t = walk.t;
+        if (kMany) place = walk;
+      }
+    }
+    __syncthreads();
+    if (unit_b < 0) return;   // (there may be fewer units than blocks)
+    prompt_unit<D>(smem, Q, K, V, qs, ks, vs, cu, Hq, Hkv, scale_log2, O, unit_b, unit_t * kTileRows, (int)(u % Hq));
+    if (!kMany || units - u <= gridDim.x) return;
+    __syncthreads();   // the next unit's tiles and place go where this one's were
+  }
+}
+
 template <int D>
 cudaError_t run(const medusa_cfg& c, const void* Q, const void* K, const void* V, int T, int64_t qs, int64_t ks, int64_t vs,
                 const int32_t* cu, void* O, cudaStream_t st) {
   const float scale_log2 = (float)(1.4426950408889634 / sqrt((double)D));
-  cudaError_t e = cudaFuncSetAttribute(prompt_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes);
+  const int units = (int)(((int64_t)T / kTileRows + c.B) * c.Hq);   // at least as many as there are
+  const bool many = c.B > kManyPrompts && units > kManyGrid;
+  const auto kernel = many ? prompt_f32_kernel<D, true> : prompt_f32_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::bytes);
   if (e != cudaSuccess) return e;
-  const int64_t units = ((int64_t)T / kTileRows + c.B) * c.Hq;   // at least as many as there are
-  e = launch_pdl(prompt_f32_kernel<D>, (unsigned)units, Smem<D>::threads, Smem<D>::bytes, st, static_cast<const float*>(Q),
+  e = launch_pdl(kernel, (unsigned)(many ? kManyGrid : units), Smem<D>::threads, Smem<D>::bytes, st, static_cast<const float*>(Q),
                  static_cast<const float*>(K), static_cast<const float*>(V), T, qs, ks, vs, cu, c.B, c.Hq, c.Hkv, scale_log2,
-                 static_cast<float*>(O));
+                 (unsigned)units, static_cast<float*>(O));
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
