@@ -375,7 +375,10 @@ MEDUSA_API int medusa_kv_store_paged(const medusa_cfg* cfg, const void* K, const
  * sequence is a tree of one node (cfg->tree_nodes = 1). All query rows that share
  * a KV head meet each tile of the prefix together; the rest is attended per
  * sequence; the partial results merge by their maxima and exp-sums ("최적화 2편"
- * (beengineer500), section 3.3). Rows past L_b in a sequence's own pages, and
+ * (beengineer500), section 3.3). Softmax and accumulation in float32; weights are
+ * rounded to bf16 before the product with V (not where a KV head has one or two
+ * rows per sequence and takes its own rows by itself). A row all of whose visible
+ * scores are -inf gives zeros. Rows past L_b in a sequence's own pages, and
  * shared rows past the longest length, never reach a result, whatever they hold.
  * A key that a row does not see never reaches it. (A value that is no number may:
  * from a shared row that another sequence has, or from a staged row of the same

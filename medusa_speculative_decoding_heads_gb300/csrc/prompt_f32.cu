@@ -5,8 +5,7 @@
 // Bound by the float32 multiply-adds (128 per SM and clock): 4 rows keys D operations. Measured
 // alone from registers they reach 68 TFLOP/s one by one and 57-61 in pairs (the registers'
 // bandwidth), but one by one they leave no issue slots for the rest, so pairs it is (prompts of
-// 700, 1, 129 and 1500 tokens, 8 heads of 64: 89 us one by one, 80 in pairs, now 76; 50
-// TFLOP/s on longer ones). A thread owns 4 rows x 8 keys of the scores and 4 rows x D / 8 head dims of O:
+// 700, 1, 129 and 1500 tokens, 8 heads of 64: 89 us one by one, 80 in pairs, now 76). A thread owns 4 rows x 8 keys of the scores and 4 rows x D / 8 head dims of O:
 // four head dims (or keys) cost it 12 shared-memory words of 16 bytes for 128 multiply-adds. A
 // half-warp's words come in one wavefront if neighbouring lanes (or every second pair) want
 // the same one, so lane bit 0 is a row's and bit 1 a key's: 24 wavefronts per warp, 40 with
@@ -15,8 +14,9 @@
 // K_{j+1} arrives while tile j's weights and values are worked on, V_j while its scores are.
 // Groups of 128 threads (3 with D = 64, 2 with D = 128: as many as registers and shared memory
 // hold tiles for) take the unit's key tiles in turn, each with its own maximum, sum and O, and
-// merge at the end: a causal prompt's last rows are its longest chain. One CTA per unit and SM,
-// those with the most keys first.
+// merge at the end: a causal prompt's last rows are its longest chain. One CTA per SM at a time and,
+// up to 64 prompts, per unit; those with the most keys first. 8192 tokens, 8 heads of 64: 1375 us, 50
+// TFLOP/s; of 128: 2665 us, 51.6; 1500 tokens 77 and 147 us (fewer than two waves of units).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -119,18 +119,18 @@ __device__ __forceinline__ void prompt_unit(float* smem, const float* __restrict
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (rg + 4 * i) * S::ld + d);
 #pragma unroll
-      for (int h = 0; h < 8; h += 4) {
+      for (int half = 0; half < 8; half += 4) {
         float4 w[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const float4*>(sk + (cg + 8 * (h + c)) * S::ld + d);
+        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const float4*>(sk + (cg + 8 * (half + c)) * S::ld + d);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[i][h + c] = __ffma2_rn(make_float2(a[i].x, a[i].y), make_float2(w[c].x, w[c].y), s[i][h + c]);
+          for (int i = 0; i < 4; ++i) s[i][half + c] = __ffma2_rn(make_float2(a[i].x, a[i].y), make_float2(w[c].x, w[c].y), s[i][half + c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[i][h + c] = __ffma2_rn(make_float2(a[i].z, a[i].w), make_float2(w[c].z, w[c].w), s[i][h + c]);
+          for (int i = 0; i < 4; ++i) s[i][half + c] = __ffma2_rn(make_float2(a[i].z, a[i].w), make_float2(w[c].z, w[c].w), s[i][half + c]);
       }
     }
     sync_group();        // K_j is no longer read

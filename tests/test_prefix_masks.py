@@ -84,3 +84,21 @@ def test_a_child_that_holds_no_numbers(shared):
     O = c.call()
     assert torch.equal(O[:, 0], O0[:, 0])
     assert bool(O[3:5, 1].isnan().all()) and torch.equal(O[5:], O0[5:]) and torch.equal(O[:3], O0[:3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,B,branching", [(8, 2, 3, (2, 2)), (8, 2, 3, (1,)), (8, 8, 24, (1,)), (16, 8, 24, (1,))])
+def test_rows_whose_scores_are_all_minus_infinity(Hq, Hkv, B, branching):
+    """A sequence whose every key scores -inf gets zeros, the others are unharmed (both kernels)."""
+    dev = gpu_ready()
+    c = Case([300 + 5 * b for b in range(B)], 0, 128, Hq, Hkv, branching, dev, seed=B, L_cap=1024)
+    c.Q[..., 0] = c.Q[..., 0].abs() + 0.5
+    O0 = c.call()
+    c.check(O0)
+    for page in c.table[1]:
+        if page >= 0:
+            c.Kp[page, ..., 0] = float("-inf")
+    c.Kt[1, ..., 0] = float("-inf")
+    O = c.call()
+    assert bool((O[1] == 0).all())
+    assert torch.equal(O[0], O0[0]) and torch.equal(O[2:], O0[2:])
