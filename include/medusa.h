@@ -336,8 +336,8 @@ MEDUSA_API int medusa_tree_attention_noalloc(const medusa_cfg* cfg, const void* 
  * the product with V. Rows of O that no sequence owns are left as they are.
  * cu_rows must not decrease: a sequence with cu_rows[b+1] < cu_rows[b] and all
  * behind it are skipped. A sequence with cu_rows[b] < 0 or cu_rows[b+1] > T is
- * skipped, too. Non-finite values stay within their own sequence (there, a value of V that is no number may reach earlier
- * rows too). O must not overlap Q, K or V. T = 0 enqueues nothing. From cfg only
+ * skipped, too. Non-finite values stay within their own sequence (there, a value
+ * of V that is no number may reach earlier rows too). O must not overlap Q, K or V. T = 0 enqueues nothing. From cfg only
  * B, Hq, Hkv, D and dtype are used (every prompt length is allowed, whatever
  * L_cap), but all of it is checked. Q, K, V, O 16-byte aligned; strides multiples
  * of 16 bytes and at least Hq * D (Hkv * D): MEDUSA_ERR_INVALID_ARG otherwise.
