@@ -454,8 +454,9 @@ MEDUSA_API int medusa_pages_compact(const medusa_cfg* cfg, void* Kp, void* Vp, i
 
 /* Failure detection. Every spin-wait of the tcgen05 kernels (the heads GEMVs, and
  * tree, prompt and prefix attention, which share the attention word: pipeline
- * mbarriers, the softmax exchanges) is bounded by a
- * clock budget of about two seconds. On expiry the waiting thread ORs a code
+ * mbarriers, the softmax exchanges) is bounded by a clock budget of about two
+ * seconds. (That covers waits, not an instruction that itself does not complete.)
+ * On expiry the waiting thread ORs a code
  * naming the wait into a device word of its kernel family, leaves its loop, and
  * the kernel returns; the GPU context stays usable, but that call's outputs are
  * invalid. The acceptance walks report the same per sequence in `flags`
