@@ -394,6 +394,78 @@ MEDUSA_API int medusa_tree_attention_prefix(const medusa_cfg* cfg, const void* Q
                                             const void* Vt, const int32_t* L, const uint64_t* anc_bits, void* O,
                                             void* workspace, medusa_stream_t stream);
 
+/* Norms of queries and keys, each head by itself, and their rotation by position,
+ * in one pass: what a projection's output goes through ahead of every attention
+ * call here. No counterpart on the pages (they take Q and K as they come).
+ *   Q, K [T] rows of [Hq][D] / [Hkv][D] elt, q_stride and k_stride elements apart
+ *   q_weight, k_weight [D] elt   y = x w / sqrt(mean(x^2) + eps) over a head's D values
+ *                                (eps finite, >= 0); NULL: those heads are not normed
+ *   inv_freq [rot_dim / 2] float angle i of a row is pos inv_freq[i], whatever the
+ *                                position to float32 precision or better
+ *   rot_dim                      head dims that turn, from the first one: a multiple of
+ *                                8 up to D (0: none; inv_freq and pos may be NULL)
+ *   pairing                      MEDUSA_ROTATE_HALVES: dims i and i + rot_dim / 2 turn
+ *                                together; MEDUSA_ROTATE_PAIRS: dims 2i and 2i + 1.
+ *                                (y_u, y_v) -> (y_u cos - y_v sin, y_v cos + y_u sin)
+ *   pos [T] int32                position of each row (for example pos [B][N] of
+ *                                medusa_tree_build; negative ones turn backwards)
+ *   Qo [T] rows of [Hq][D], qo_stride apart; Ko [T] rows of [Hkv][D], ko_stride
+ *                                apart, or with ko_stride = 0 the staged layout
+ *                                [B][Hkv][N][D] of the tree calls (T must be B * N,
+ *                                row b * N + n)
+ * All in float32 (squares and their sum too), rounded once at the end. In place
+ * (Qo = Q, Ko = K, same strides) is allowed; any other overlap is not. From cfg
+ * B, Hq, Hkv, D, dtype and the tree are used, all of it is checked. Pointers but
+ * pos 16-byte aligned; strides as for medusa_prompt_attention
+ * (MEDUSA_ERR_INVALID_ARG otherwise). rot_dim no multiple of 8, or T (Hq / 4 +
+ * Hkv / 4 + 2) above 2^31 - 1: MEDUSA_ERR_UNSUPPORTED. T = 0 enqueues nothing. */
+enum { MEDUSA_ROTATE_HALVES = 0, MEDUSA_ROTATE_PAIRS = 1 };
+MEDUSA_API int medusa_qk_norm_rotate(const medusa_cfg* cfg, const void* Q, const void* K, int32_t T, int64_t q_stride,
+                                     int64_t k_stride, const void* q_weight, const void* k_weight, float eps,
+                                     const float* inv_freq, int32_t rot_dim, int32_t pairing, const int32_t* pos, void* Qo,
+                                     void* Ko, int64_t qo_stride, int64_t ko_stride, medusa_stream_t stream);
+
+/* Attention of new tokens over a paged cache: a prompt taken in chunks, single
+ * tokens, or both in one batch. What "Speculative Decoding 원리와 가속 아키텍처"
+ * (blog.huny.dev), section 3, decodes with; the call has no counterpart there.
+ *   Q [T] rows of [Hq][D] elt, q_stride elements from row to row
+ *   cu_rows [B+1] int32        sequence b owns rows [cu_rows[b], cu_rows[b+1])
+ *   start [B] int32            logical row that sequence b's row 0 is; NULL: 0
+ *   Kp, Vp, num_pages, page_rows, block_table   as for medusa_tree_attention_paged
+ *                              (any dtype and D), the new tokens' keys and values
+ *                              among them (medusa_kv_store_paged takes the same
+ *                              cu_rows and start)
+ *   O [T][Hq][D] elt, dense    row i of a sequence, logical row p = start[b] + i:
+ *                              softmax over logical rows 0..p of q.k / sqrt(D),
+ *                              times v; KV head of query head h is h / (Hq / Hkv)
+ * Softmax and accumulation in float32; bf16 weights are rounded to bf16 before
+ * the product with V. Rows of O that no sequence owns are left as they are, and so
+ * are those of a sequence that is skipped: cu_rows as for medusa_prompt_attention,
+ * or start[b] < 0, or start[b] + its rows > L_cap. Block-table entries past a
+ * sequence's last page are not read; a page id outside [0, num_pages) stands for
+ * rows of zeros. Cache rows that no row of a sequence sees may hold anything. (Among
+ * rows of one sequence, a value of V that is no number may reach rows that do not see
+ * it, from keys that other rows of the same call see.) A row all of whose visible
+ * scores are -inf gives no number. O must not overlap an input. T = 0 enqueues nothing.
+ * Alignment and q_stride as for medusa_prompt_attention; (num_pages + 1) * Hkv above
+ * 2^31 - 1: MEDUSA_ERR_UNSUPPORTED. The workspace has medusa_chunk_workspace_size()
+ * bytes (256-byte aligned; NULL will do for 0) for T rows; each call writes all of it
+ * that it reads, so calls one after the other may share it, and calls that may overlap
+ * may not.
+ * medusa_window_attention_paged: the same with a sliding window and first rows that
+ * stay visible: row p sees the rows j <= p with j > p - window or j < sinks (window
+ * >= 1, sinks >= 0; MEDUSA_ERR_INVALID_ARG otherwise). Block-table entries of pages
+ * that no row sees are not read: such pages may have been given back. */
+MEDUSA_API int medusa_chunk_workspace_size(const medusa_cfg* cfg, int32_t T, size_t* bytes);
+MEDUSA_API int medusa_chunk_attention_paged(const medusa_cfg* cfg, const void* Q, int32_t T, int64_t q_stride,
+                                            const int32_t* cu_rows, const int32_t* start, const void* Kp, const void* Vp,
+                                            int32_t num_pages, int32_t page_rows, const int32_t* block_table, void* O,
+                                            void* workspace, medusa_stream_t stream);
+MEDUSA_API int medusa_window_attention_paged(const medusa_cfg* cfg, const void* Q, int32_t T, int64_t q_stride,
+                                             const int32_t* cu_rows, const int32_t* start, const void* Kp, const void* Vp,
+                                             int32_t num_pages, int32_t page_rows, const int32_t* block_table, int32_t window,
+                                             int32_t sinks, void* O, void* workspace, medusa_stream_t stream);
+
 /* Pages of a cache: who holds them, on the device.
  *   block_table [B][L_cap / page_rows] int32   page ids; a negative entry holds no page
  *   refs [num_pages] int32                     how many block-table entries hold a page

@@ -28,8 +28,10 @@ ENTRY_POINTS = ("medusa_node_count", "medusa_workspace_size", "medusa_heads", "m
                 "medusa_selftest_wait_timeout", "medusa_checked_build", "medusa_poll_checks", "medusa_step_fused",
                 "medusa_prompt_attention", "medusa_kv_store_paged", "medusa_prefix_workspace_size",
                 "medusa_tree_attention_prefix", "medusa_pages_workspace_size", "medusa_pages_reserve",
-                "medusa_pages_fork", "medusa_pages_free", "medusa_pages_compact",
+                "medusa_pages_fork", "medusa_pages_free", "medusa_pages_compact", "medusa_qk_norm_rotate",
+                "medusa_chunk_workspace_size", "medusa_chunk_attention_paged", "medusa_window_attention_paged",
                 "medusa_launch_count", "medusa_status_string")
+ROTATE_HALVES, ROTATE_PAIRS = 0, 1
 CHECK_TOKEN, CHECK_TREE, CHECK_PATH, CHECK_PAGE = 1, 2, 4, 8
 
 
@@ -124,6 +126,10 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         "medusa_pages_fork": [cp, P, P, i32, i32, i32, ctypes.c_size_t, i32, P, P, P, P, P, P, P, P],
         "medusa_pages_free": [cp, i32, i32, i32, P, P, P, P, P],
         "medusa_pages_compact": [cp, P, P, i32, i32, i32, ctypes.c_size_t, P, P, P, P, P, P],
+        "medusa_qk_norm_rotate": [cp, P, P, i32, i64, i64, P, P, ctypes.c_float, P, i32, i32, P, P, P, i64, i64, P],
+        "medusa_chunk_workspace_size": [cp, i32, ctypes.POINTER(ctypes.c_size_t)],
+        "medusa_chunk_attention_paged": [cp, P, i32, i64, P, P, P, P, i32, i32, P, P, P, P],
+        "medusa_window_attention_paged": [cp, P, i32, i64, P, P, P, P, i32, i32, P, i32, i32, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -394,6 +400,38 @@ def pages_compact(cfg, Kp, Vp, num_pages, page_rows, n_layers, pool_layer_elems,
     _check("medusa_pages_compact", load().medusa_pages_compact(
         ctypes.byref(cfg), _ptr(Kp), _ptr(Vp), int(num_pages), int(page_rows), int(n_layers), int(pool_layer_elems),
         _ptr(block_table), _ptr(refs), _ptr(page_map), _ptr(n_live), _ptr(workspace), _stream(stream)))
+
+
+def qk_norm_rotate(cfg, Q, K, T, q_stride, k_stride, q_weight, k_weight, eps, inv_freq, rot_dim, pairing, pos, Qo, Ko,
+                   qo_stride, ko_stride, stream=None):
+    """Norms of queries and keys by head and their rotation by position; a weight may be None (no norm), ``ko_stride`` 0 is
+    the staged layout of the tree calls."""
+    _check("medusa_qk_norm_rotate", load().medusa_qk_norm_rotate(
+        ctypes.byref(cfg), _ptr(Q), _ptr(K), int(T), int(q_stride), int(k_stride), _ptr(q_weight), _ptr(k_weight), float(eps),
+        _ptr(inv_freq), int(rot_dim), int(pairing), _ptr(pos), _ptr(Qo), _ptr(Ko), int(qo_stride), int(ko_stride),
+        _stream(stream)))
+
+
+def chunk_workspace_size(cfg, T: int) -> int:
+    n = ctypes.c_size_t()
+    _check("medusa_chunk_workspace_size", load().medusa_chunk_workspace_size(ctypes.byref(cfg), int(T), ctypes.byref(n)))
+    return n.value
+
+
+def chunk_attention_paged(cfg, Q, T, q_stride, cu_rows, start, Kp, Vp, num_pages, page_rows, block_table, O, workspace,
+                          stream=None):
+    """Attention of packed new tokens over the pages that hold them and all before; ``start`` may be None (0)."""
+    _check("medusa_chunk_attention_paged", load().medusa_chunk_attention_paged(
+        ctypes.byref(cfg), _ptr(Q), int(T), int(q_stride), _ptr(cu_rows), _ptr(start), _ptr(Kp), _ptr(Vp), int(num_pages),
+        int(page_rows), _ptr(block_table), _ptr(O), _ptr(workspace), _stream(stream)))
+
+
+def window_attention_paged(cfg, Q, T, q_stride, cu_rows, start, Kp, Vp, num_pages, page_rows, block_table, window, sinks, O,
+                           workspace, stream=None):
+    """chunk_attention_paged whose rows see the last ``window`` rows and the first ``sinks`` only."""
+    _check("medusa_window_attention_paged", load().medusa_window_attention_paged(
+        ctypes.byref(cfg), _ptr(Q), int(T), int(q_stride), _ptr(cu_rows), _ptr(start), _ptr(Kp), _ptr(Vp), int(num_pages),
+        int(page_rows), _ptr(block_table), int(window), int(sinks), _ptr(O), _ptr(workspace), _stream(stream)))
 
 
 def raw_call(name: str, *args) -> int:

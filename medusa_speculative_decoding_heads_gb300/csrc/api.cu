@@ -3,7 +3,9 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 
+#include "chunk.cuh"
 #include "common.cuh"
 
 namespace medusa {
@@ -95,6 +97,40 @@ int check_prefix(const medusa_cfg& c, int shared_rows) {
   if (c.dtype != MEDUSA_BF16 || c.D != 128) return MEDUSA_ERR_UNSUPPORTED;
   if (shared_rows % 128 != 0 || shared_rows > c.L_cap) return MEDUSA_ERR_UNSUPPORTED;
   return MEDUSA_OK;
+}
+
+// The checks of attention over a paged cache, and the call itself.
+int chunk_attention(const medusa_cfg* cfg, const void* Q, int T, int64_t q_stride, const int32_t* cu_rows, const int32_t* start,
+                    const void* Kp, const void* Vp, int num_pages, int page_rows, const int32_t* block_table, int window, int sinks,
+                    void* O, void* workspace, cudaStream_t stream) {
+  int s = check_cfg(cfg);
+  if (s == MEDUSA_OK) s = check_pages(*cfg, num_pages, page_rows);
+  if (s != MEDUSA_OK) return s;
+  if (T < 0 || window < 1 || sinks < 0) return MEDUSA_ERR_INVALID_ARG;
+  if (T == 0) return MEDUSA_OK;
+  if (!Q || !cu_rows || !Kp || !Vp || !block_table || !O || (!workspace && chunk_workspace(*cfg, T) > 0))
+    return MEDUSA_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(Kp) || !aligned16(Vp) || !aligned16(O) || !aligned256(workspace)) return MEDUSA_ERR_INVALID_ARG;
+  if (!row_stride_ok(*cfg, q_stride, cfg->Hq)) return MEDUSA_ERR_INVALID_ARG;
+  if (((int64_t)num_pages + 1) * cfg->Hkv > INT32_MAX) return MEDUSA_ERR_UNSUPPORTED;   // page planes are counted in 32 bits
+  ChunkArgs a{};
+  a.cu = cu_rows;
+  a.start = start;
+  a.table = block_table;
+  a.B = cfg->B;
+  a.T = T;
+  a.Hq = cfg->Hq;
+  a.Hkv = cfg->Hkv;
+  a.L_cap = cfg->L_cap;
+  a.page_rows = page_rows;
+  a.max_pages = cfg->L_cap / page_rows;
+  a.num_pages = num_pages;
+  a.window = window;
+  a.sinks = sinks;
+  a.q_stride = q_stride;
+  a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cfg->D));
+  const cudaError_t e = launch_chunk_attention(*cfg, Q, Kp, Vp, O, a, workspace, stream);
+  return e == cudaSuccess ? MEDUSA_OK : MEDUSA_ERR_CUDA;
 }
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? MEDUSA_OK : MEDUSA_ERR_CUDA; }
@@ -308,6 +344,54 @@ int medusa_tree_attention_prefix(const medusa_cfg* cfg, const void* Q, const voi
                                            Vt, L, anc_bits, O, workspace, (cudaStream_t)stream));
 }
 
+int medusa_qk_norm_rotate(const medusa_cfg* cfg, const void* Q, const void* K, int32_t T, int64_t q_stride, int64_t k_stride,
+                          const void* q_weight, const void* k_weight, float eps, const float* inv_freq, int32_t rot_dim,
+                          int32_t pairing, const int32_t* pos, void* Qo, void* Ko, int64_t qo_stride, int64_t ko_stride,
+                          medusa_stream_t stream) {
+  int s = check_cfg(cfg);
+  if (s != MEDUSA_OK) return s;
+  if (T < 0 || rot_dim < 0 || rot_dim > cfg->D || !(eps >= 0.f) || !std::isfinite(eps)) return MEDUSA_ERR_INVALID_ARG;
+  if (pairing != MEDUSA_ROTATE_HALVES && pairing != MEDUSA_ROTATE_PAIRS) return MEDUSA_ERR_INVALID_ARG;
+  if (rot_dim % 8 != 0) return MEDUSA_ERR_UNSUPPORTED;
+  if (T == 0) return MEDUSA_OK;
+  if (!Q || !K || !Qo || !Ko || (rot_dim > 0 && (!inv_freq || !pos))) return MEDUSA_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(Qo) || !aligned16(Ko) || !aligned16(q_weight) || !aligned16(k_weight) ||
+      !aligned16(inv_freq))
+    return MEDUSA_ERR_INVALID_ARG;
+  if (!row_stride_ok(*cfg, q_stride, cfg->Hq) || !row_stride_ok(*cfg, k_stride, cfg->Hkv) ||
+      !row_stride_ok(*cfg, qo_stride, cfg->Hq) || (ko_stride != 0 && !row_stride_ok(*cfg, ko_stride, cfg->Hkv)))
+    return MEDUSA_ERR_INVALID_ARG;
+  if (ko_stride == 0 && ((int64_t)T != (int64_t)cfg->B * tree_shape(*cfg).N || Ko == K)) return MEDUSA_ERR_INVALID_ARG;
+  if ((Qo == Q && qo_stride != q_stride) || (Ko == K && ko_stride != k_stride)) return MEDUSA_ERR_INVALID_ARG;
+  // blocks are counted in 32 bits (a token's heads go to Hq / 4 + Hkv / 4 + 2 groups at most, a group to 32 lanes at most)
+  if ((int64_t)T * (cfg->Hq / 4 + cfg->Hkv / 4 + 2) > (int64_t)INT32_MAX) return MEDUSA_ERR_UNSUPPORTED;
+  return from_cuda(launch_qk_norm_rotate(*cfg, Q, K, T, q_stride, k_stride, q_weight, k_weight, eps, inv_freq, rot_dim, pairing,
+                                         pos, Qo, Ko, qo_stride, ko_stride, (cudaStream_t)stream));
+}
+
+int medusa_chunk_workspace_size(const medusa_cfg* cfg, int32_t T, size_t* bytes) {
+  int s = check_cfg(cfg);
+  if (s != MEDUSA_OK) return s;
+  if (!bytes || T < 0) return MEDUSA_ERR_INVALID_ARG;
+  *bytes = T > 0 ? chunk_workspace(*cfg, T) : 0;
+  return MEDUSA_OK;
+}
+
+int medusa_chunk_attention_paged(const medusa_cfg* cfg, const void* Q, int32_t T, int64_t q_stride, const int32_t* cu_rows,
+                                 const int32_t* start, const void* Kp, const void* Vp, int32_t num_pages, int32_t page_rows,
+                                 const int32_t* block_table, void* O, void* workspace, medusa_stream_t stream) {
+  return chunk_attention(cfg, Q, T, q_stride, cu_rows, start, Kp, Vp, num_pages, page_rows, block_table, INT32_MAX, 0, O, workspace,
+                         (cudaStream_t)stream);
+}
+
+int medusa_window_attention_paged(const medusa_cfg* cfg, const void* Q, int32_t T, int64_t q_stride, const int32_t* cu_rows,
+                                  const int32_t* start, const void* Kp, const void* Vp, int32_t num_pages, int32_t page_rows,
+                                  const int32_t* block_table, int32_t window, int32_t sinks, void* O, void* workspace,
+                                  medusa_stream_t stream) {
+  return chunk_attention(cfg, Q, T, q_stride, cu_rows, start, Kp, Vp, num_pages, page_rows, block_table, window, sinks, O, workspace,
+                         (cudaStream_t)stream);
+}
+
 int medusa_pages_workspace_size(const medusa_cfg* cfg, int32_t num_pages, size_t* bytes) {
   int s = check_cfg(cfg);
   if (s != MEDUSA_OK) return s;
@@ -474,16 +558,17 @@ int medusa_checked_build(void) {
 
 int medusa_poll_checks(medusa_stream_t stream, uint32_t* codes) {
   cudaStream_t st = (cudaStream_t)stream;
-  uint32_t w[6] = {0, 0, 0, 0, 0, 0};
+  uint32_t w[7] = {0, 0, 0, 0, 0, 0, 0};
   cudaError_t e = tree_take_checks(&w[0], st);
   if (e == cudaSuccess) e = verify_take_checks(&w[1], st);
   if (e == cudaSuccess) e = compact_take_checks(&w[2], st);
   if (e == cudaSuccess) e = attention_tc_take_checks(&w[3], st);
   if (e == cudaSuccess) e = pages_take_checks(&w[4], st);
   if (e == cudaSuccess) e = rows_tc_take_checks(&w[5], st);
+  if (e == cudaSuccess) e = chunk_take_checks(&w[6], st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return MEDUSA_ERR_CUDA;
-  const uint32_t all = w[0] | w[1] | w[2] | w[3] | w[4] | w[5];
+  const uint32_t all = w[0] | w[1] | w[2] | w[3] | w[4] | w[5] | w[6];
   if (codes) *codes = all;
   return all ? MEDUSA_ERR_BOUNDS : MEDUSA_OK;
 }

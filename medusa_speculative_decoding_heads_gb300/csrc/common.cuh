@@ -180,6 +180,12 @@ cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const vo
                                     const void* Vt, const int32_t* L, const uint64_t* bits, void* O, void* ws,
                                     cudaStream_t st);
 
+// Norms of queries and keys and their rotation (rotate.cu).
+cudaError_t launch_qk_norm_rotate(const medusa_cfg& c, const void* Q, const void* K, int T, int64_t q_stride, int64_t k_stride,
+                                  const void* q_weight, const void* k_weight, float eps, const float* inv_freq, int rot_dim,
+                                  int pairing, const int32_t* pos, void* Qo, void* Ko, int64_t qo_stride, int64_t ko_stride,
+                                  cudaStream_t st);
+
 // Pages of a cache (pages.cu).
 size_t pages_workspace(const medusa_cfg& c, int num_pages);
 cudaError_t launch_pages_reserve(const medusa_cfg& c, int num_pages, int page_rows, const int32_t* rows, int32_t* table,
@@ -244,6 +250,7 @@ cudaError_t compact_take_checks(uint32_t* out, cudaStream_t st);
 cudaError_t attention_tc_take_checks(uint32_t* out, cudaStream_t st);
 cudaError_t pages_take_checks(uint32_t* out, cudaStream_t st);
 cudaError_t rows_tc_take_checks(uint32_t* out, cudaStream_t st);
+cudaError_t chunk_take_checks(uint32_t* out, cudaStream_t st);
 
 // Configuration checks shared by every entry point (MEDUSA_OK or an error status).
 int check_cfg_public(const medusa_cfg* c);

@@ -1,0 +1,209 @@
+// Norms of queries and keys, each head by itself, and their rotation by position, in one pass.
+//
+// y = x w / sqrt(mean(x^2) + eps); then pairs (y_u, y_v) of the first R head dims turn by the angle
+// a = pos f_i: (y_u cos a - y_v sin a, y_v cos a + y_u sin a). Bound by the bytes of Q and K, read
+// once and written once.
+//
+// D / 8 lanes hold a head, 8 head dims each, in two pieces of 4 that lie so that both dims of a pair
+// are in the same lane: R / 2 apart where halves turn against each other, next to each other where
+// neighbours do. A group of such lanes takes up to kHeads<T> heads of one token: all of them are on
+// their way while the lane works out its 4 angles, which the heads share.
+//
+// Angles. pos f in float32 is off by 2^-25 pos f, 0.03 at a position of a million; here f / 2 pi
+// becomes a 64-bit fraction of a turn (from a product in 64 bits: off by 2^-52 f), so that pos times it
+// modulo 2^64 is the exact remainder. Its nearest quarter turn is taken off, and the rest, |a| <=
+// pi / 4, goes into the Taylor series of sine and cosine (to a^9 and a^10: off by 2e-9 and 2e-10).
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace medusa {
+namespace {
+
+constexpr int kThreads = 128;
+template <typename T> constexpr int kHeads = sizeof(T) == 2 ? 8 : 4;   // heads of a group: 32 registers on their way
+
+struct RotateArgs {
+  const void *Q, *K, *qw, *kw;
+  void *Qo, *Ko;
+  int64_t qs, ks, qos, kos;   // elements from row to row; kos 0: the trees' staged layout
+  const float* freq;
+  const int32_t* pos;
+  int64_t groups;             // T * (groups of a token)
+  int per_token, q_groups;    // groups of a token, and how many of them are the queries'
+  int Hq, Hkv, N, R, pairs;
+  float eps;
+};
+
+// 4 values, unpacked.
+__device__ __forceinline__ float4 get4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 get4(const uint16_t* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void put4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void put4(uint16_t* p, const float4& v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+}
+
+// (cos, sin) of pos * freq.
+__device__ __forceinline__ float2 turn_of(float freq, int pos) {
+  double t = (double)freq * 0.15915494309189533577;   // turns per position: f / 2 pi
+  t -= rint(t);
+  if (!(fabs(t) <= 0.5)) return make_float2(NAN, NAN);   // (a frequency that is no finite number)
+  const uint64_t turns = (uint64_t)__double2ll_rn(t * 9223372036854775808.0) * 2u * (uint64_t)(int64_t)pos;   // 2^64 to a turn
+  const int h = (int)(turns >> 32), quarter = (int)((uint32_t)h + (1u << 29)) >> 30;
+  const int rest = (int)((uint32_t)h - ((uint32_t)quarter << 30));
+  const float a = (float)rest * 1.4629180792671596e-9f;   // pi 2^-31
+  const float s2 = a * a;
+  float s = fmaf(s2, 2.7557319e-6f, -1.9841270e-4f);
+  s = fmaf(s2, s, 8.3333333e-3f);
+  s = fmaf(s2, s, -1.6666667e-1f);
+  s = fmaf(a * s2, s, a);
+  float c = fmaf(s2, -2.7557319e-7f, 2.4801587e-5f);
+  c = fmaf(s2, c, -1.3888889e-3f);
+  c = fmaf(s2, c, 4.1666667e-2f);
+  c = fmaf(s2, c, -0.5f);
+  c = fmaf(s2, c, 1.f);
+  const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;   // a quarter turn on: (c, s) -> (-s, c)
+  return make_float2(((quarter + 1) & 2) ? -x : x, (quarter & 2) ? -y : y);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+qk_norm_rotate_kernel(const RotateArgs a) {
+  constexpr int kLanes = D / 8, H = kHeads<T>;
+  const int l = threadIdx.x % kLanes;
+  const int64_t g = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;
+  pdl_wait();
+  pdl_trigger();
+  if (g >= a.groups) return;   // (whole groups: the shuffles below name a group's lanes only)
+  const unsigned mask = (kLanes == 32 ? 0xffffffffu : ((1u << kLanes) - 1u)) << ((threadIdx.x & 31) / kLanes * kLanes);
+  const int64_t t = g / a.per_token;
+  const int of = (int)(g - t * a.per_token);
+  const bool isq = of < a.q_groups;
+  const int h0 = (isq ? of : of - a.q_groups) * H, heads = min(H, (isq ? a.Hq : a.Hkv) - h0);
+  // the lane's two pieces
+  const bool turns = 8 * l < a.R;
+  const int c0 = a.pairs ? 8 * l : turns ? 4 * l : 8 * l, c1 = a.pairs || !turns ? c0 + 4 : (a.R >> 1) + 4 * l;
+  const T* src = static_cast<const T*>(isq ? a.Q : a.K) + t * (isq ? a.qs : a.ks) + (int64_t)h0 * D;
+  float4 x0[H], x1[H];
+#pragma unroll
+  for (int i = 0; i < H; ++i)
+    if (i < heads) {
+      x0[i] = get4(src + i * D + c0);
+      x1[i] = get4(src + i * D + c1);
+    }
+  const T* w = static_cast<const T*>(isq ? a.qw : a.kw);
+  float4 w0, w1;
+  if (w) {
+    w0 = get4(w + c0);
+    w1 = get4(w + c1);
+  }
+  float2 cs[4];
+  if (turns) {
+    const int pos = a.pos[t];
+    const float4 f = *reinterpret_cast<const float4*>(a.freq + 4 * l);
+    cs[0] = turn_of(f.x, pos);
+    cs[1] = turn_of(f.y, pos);
+    cs[2] = turn_of(f.z, pos);
+    cs[3] = turn_of(f.w, pos);
+  }
+  T* dst;
+  int64_t step = D;
+  if (isq) {
+    dst = static_cast<T*>(a.Qo) + t * a.qos + (int64_t)h0 * D;
+  } else if (a.kos) {
+    dst = static_cast<T*>(a.Ko) + t * a.kos + (int64_t)h0 * D;
+  } else {
+    const int64_t b = t / a.N;
+    dst = static_cast<T*>(a.Ko) + ((b * a.Hkv + h0) * a.N + (t - b * a.N)) * D;
+    step = (int64_t)a.N * D;
+  }
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    if (i >= heads) break;
+    float4 &u = x0[i], &v = x1[i];
+    if (w) {
+      float s = u.x * u.x;
+      s = fmaf(u.y, u.y, s);
+      s = fmaf(u.z, u.z, s);
+      s = fmaf(u.w, u.w, s);
+      s = fmaf(v.x, v.x, s);
+      s = fmaf(v.y, v.y, s);
+      s = fmaf(v.z, v.z, s);
+      s = fmaf(v.w, v.w, s);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
+      const float r = rsqrtf(fmaf(s, 1.f / D, a.eps));
+      u = make_float4(u.x * r * w0.x, u.y * r * w0.y, u.z * r * w0.z, u.w * r * w0.w);
+      v = make_float4(v.x * r * w1.x, v.y * r * w1.y, v.z * r * w1.z, v.w * r * w1.w);
+    }
+    if (turns) {
+      auto turn = [](float& p, float& q, const float2& c) {
+        const float x = p * c.x - q * c.y;
+        q = q * c.x + p * c.y;
+        p = x;
+      };
+      if (a.pairs) {
+        turn(u.x, u.y, cs[0]);
+        turn(u.z, u.w, cs[1]);
+        turn(v.x, v.y, cs[2]);
+        turn(v.z, v.w, cs[3]);
+      } else {
+        turn(u.x, v.x, cs[0]);
+        turn(u.y, v.y, cs[1]);
+        turn(u.z, v.z, cs[2]);
+        turn(u.w, v.w, cs[3]);
+      }
+    }
+    put4(dst + i * step + c0, u);
+    put4(dst + i * step + c1, v);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_rotate(const medusa_cfg& c, const void* Q, const void* K, int T, int64_t q_stride, int64_t k_stride,
+                                  const void* q_weight, const void* k_weight, float eps, const float* inv_freq, int rot_dim,
+                                  int pairing, const int32_t* pos, void* Qo, void* Ko, int64_t qo_stride, int64_t ko_stride,
+                                  cudaStream_t st) {
+  const int H = c.dtype == MEDUSA_F32 ? kHeads<float> : kHeads<uint16_t>;
+  RotateArgs a{};
+  a.Q = Q;
+  a.K = K;
+  a.qw = q_weight;
+  a.kw = k_weight;
+  a.Qo = Qo;
+  a.Ko = Ko;
+  a.qs = q_stride;
+  a.ks = k_stride;
+  a.qos = qo_stride;
+  a.kos = ko_stride;
+  a.freq = inv_freq;
+  a.pos = pos;
+  a.q_groups = (c.Hq + H - 1) / H;
+  a.per_token = a.q_groups + (c.Hkv + H - 1) / H;
+  a.groups = (int64_t)T * a.per_token;
+  a.Hq = c.Hq;
+  a.Hkv = c.Hkv;
+  a.N = tree_shape(c).N;
+  a.R = rot_dim;
+  a.pairs = pairing == MEDUSA_ROTATE_PAIRS;
+  a.eps = eps;
+  const int per_block = kThreads * 8 / c.D;
+  const auto kernel = c.dtype == MEDUSA_F32 ? (c.D == 64 ? qk_norm_rotate_kernel<float, 64> : qk_norm_rotate_kernel<float, 128>)
+                                            : (c.D == 64 ? qk_norm_rotate_kernel<uint16_t, 64> : qk_norm_rotate_kernel<uint16_t, 128>);
+  const cudaError_t e = launch_pdl(kernel, (unsigned)((a.groups + per_block - 1) / per_block), kThreads, 0, st, a);
+  note_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace medusa

@@ -72,6 +72,52 @@ def prefix_attention(Q, Kp, Vp, P: int, prefix: Sequence[int], shared: int, tabl
     return O, A, S
 
 
+def chunk_attention(Q, Kp, Vp, P: int, table, cu: Sequence[int], start, L_cap: int, window=None, sinks: int = 0):
+    """New tokens over the pages that hold them and all before: (O, A, S) as ``attend``, [T][Hq][D] and [T][Hq], and
+    the rows that are computed, [T] bool. A page outside the pool stands for zeros."""
+    T, Hq, D = Q.shape
+    O = torch.zeros((T, Hq, D), dtype=torch.float64, device=Q.device)
+    A, S = torch.zeros_like(O), torch.zeros((T, Hq), dtype=torch.float64, device=Q.device)
+    owned = torch.zeros(T, dtype=torch.bool, device=Q.device)
+    for b, (a, e) in enumerate(zip(cu[:-1], cu[1:])):
+        if e < a:
+            break
+        s = int(start[b]) if start is not None else 0
+        if a < 0 or e == a or e > T or s < 0 or s + e - a > L_cap:
+            continue
+        key = [j for j in range(s + e - a) if window is None or j < sinks or j > s - window]   # what any row sees
+        pages = torch.tensor([int(table[b][j // P]) for j in key], dtype=torch.long, device=Q.device)
+        j = torch.tensor(key, dtype=torch.long, device=Q.device)
+        held = (pages >= 0) & (pages < Kp.shape[0])
+        k, v = (torch.where(held[:, None, None], pool[pages.clamp(0, Kp.shape[0] - 1), :, j % P], 0.0) for pool in (Kp, Vp))
+        p = torch.arange(s, s + e - a, device=Q.device)[:, None]
+        see = j <= p
+        if window is not None:
+            see = see & ((j > p - window) | (j < sinks))
+        O[a:e], A[a:e], S[a:e] = attend(Q[a:e], k, v, see)
+        owned[a:e] = True
+    return O, A, S, owned
+
+
+def norm_rotate(x, weight, eps: float, inv_freq, rot: int, pairs: bool, pos):
+    """Heads x [T][H][D] normed and turned in float64: (y, M): the result and, for each value, what multiplies the
+    relative errors of the norm, the sine and the cosine: |y_u| + |y_v| of its pair before it turns."""
+    y = x.double()
+    if weight is not None:
+        y = y / torch.sqrt((y * y).mean(-1, keepdim=True) + eps) * weight.double()
+    M = y.abs()
+    if rot == 0:
+        return y, M
+    a = pos.double()[:, None] * inv_freq.double()[None]
+    cos, sin = torch.cos(a)[:, None], torch.sin(a)[:, None]
+    out = y.clone()
+    u, v = (slice(0, rot, 2), slice(1, rot, 2)) if pairs else (slice(0, rot // 2), slice(rot // 2, rot))
+    out[..., u], out[..., v] = y[..., u] * cos - y[..., v] * sin, y[..., v] * cos + y[..., u] * sin
+    both = M[..., u] + M[..., v]
+    M[..., u], M[..., v] = both, both.clone()
+    return out, M
+
+
 class Pages:
     """Block tables, reference counts, lengths and (optionally) pools [layers][pages][Hkv][P][D]."""
 
