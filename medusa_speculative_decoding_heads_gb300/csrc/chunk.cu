@@ -70,16 +70,108 @@ cudaError_t run(const void* Q, const void* Kp, const void* Vp, void* O, const Ch
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Joins the partial results of the units that were cut: O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s, a warp
+// per row, kMergeRows rows of a unit per CTA. Bound by the partial results' bytes, which lie in L2.
+constexpr int kMergeThreads = 256, kMergeRows = 32;
+
+template <int X>
+struct Vec;
+template <>
+struct Vec<2> { using type = float2; };
+template <>
+struct Vec<4> { using type = float4; };
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads)
+chunk_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml_part, const ChunkCut* __restrict__ cuts,
+                   const ChunkSpace sp, int Hq, T* __restrict__ O) {
+  constexpr int X = D / 32;
+  using V = typename Vec<X>::type;
+  pdl_wait();
+  pdl_trigger();
+  const bool pair = (int)blockIdx.x < sp.pair_streams;
+  const int stream = pair ? (int)blockIdx.x : (int)blockIdx.x - sp.pair_streams;
+  const ChunkCut cut = cuts[blockIdx.x];
+  if (cut.parts == 0) return;
+  const int rows = pair ? sp.pair_rows : sp.single_rows, along = pair ? sp.npos : sp.single_npos, lane = threadIdx.x & 31;
+  const int tile_rows = along << sp.gp_shift;
+  for (int r = blockIdx.y * kMergeRows + (threadIdx.x >> 5); r < min(rows, (int)(blockIdx.y + 1) * kMergeRows); r += kMergeThreads / 32) {
+    const int tile = r / tile_rows, head = (r - tile * tile_rows) / along, pos = r - tile * tile_rows - head * along + tile * along;
+    if (pos >= cut.left) continue;
+    float M = -INFINITY, sum = 0.f, acc[X] = {};
+    for (int s = 0; s <= cut.parts; ++s) {
+      const int64_t at = (pair ? sp.pair_part(stream + s, s == 0) : sp.single_part(stream + s, s == 0)) + r;
+      const float2 ml = *reinterpret_cast<const float2*>(ml_part + 2 * at);
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;   // nothing was visible: its O need not have been written
+      const V v = *reinterpret_cast<const V*>(o_part + at * D + X * lane);
+      const float* o = reinterpret_cast<const float*>(&v);
+      const float mn = fmaxf(M, ml.x), mu = mn == -INFINITY ? 0.f : mn, w0 = exp2f(M - mu), w1 = exp2f(ml.x - mu);
+      M = mn;
+      sum = sum * w0 + ml.y * w1;
+#pragma unroll
+      for (int x = 0; x < X; ++x) acc[x] = acc[x] * w0 + o[x] * w1;
+    }
+    const float inv = 1.f / sum;   // (0 where every visible score is -inf: no number)
+    T* op = O + ((size_t)(cut.pos0 + pos) * Hq + cut.h0 + head) * D + X * lane;
+    if constexpr (sizeof(T) == 4) {
+      V v;
+#pragma unroll
+      for (int x = 0; x < X; ++x) reinterpret_cast<float*>(&v)[x] = acc[x] * inv;
+      *reinterpret_cast<V*>(op) = v;
+    } else {
+#pragma unroll
+      for (int x = 0; x < X; x += 2) {
+        uint32_t w;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(acc[x + 1] * inv), "f"(acc[x] * inv));
+        reinterpret_cast<uint32_t*>(op)[x / 2] = w;
+      }
+    }
+  }
+}
+
+template <typename T, int D>
+cudaError_t merge(const medusa_cfg& c, void* O, const ChunkSpace& sp, void* ws, cudaStream_t st) {
+  const int rows = sp.pair_streams ? sp.pair_rows : sp.single_rows;
+  const dim3 grid(sp.pair_streams + sp.streams, (rows + kMergeRows - 1) / kMergeRows);
+  const char* base = static_cast<const char*>(ws);
+  const cudaError_t e = launch_pdl(chunk_merge_kernel<T, D>, grid, kMergeThreads, 0, st, reinterpret_cast<const float*>(base),
+                                   reinterpret_cast<const float*>(base + sp.ml), reinterpret_cast<const ChunkCut*>(base + sp.cuts), sp,
+                                   c.Hq, static_cast<T*>(O));
+  note_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 }  // namespace
 
 MEDUSA_CHECK_TAKE(chunk_take_checks)
 
-size_t chunk_workspace(const medusa_cfg&, int) { return 0; }
+ChunkSpace chunk_space(const medusa_cfg& c, int T) {
+  constexpr int kSms = 152, kRows = 128;
+  ChunkSpace sp{};
+  const int G = c.Hq / c.Hkv;
+  while (sp.gp_shift < 4 && G % (2 << sp.gp_shift) == 0) ++sp.gp_shift;   // the largest power of two that divides the group
+  sp.npos = kRows >> sp.gp_shift;
+  sp.pair_streams = T > sp.npos ? kSms : 0;   // (no sequence has more rows than there are)
+  sp.pair_rows = 2 * kRows;
+  sp.streams = 2 * kSms;
+  sp.single_npos = T < sp.npos ? T : sp.npos;
+  sp.single_rows = sp.single_npos << sp.gp_shift;
+  const size_t rows = (size_t)2 * sp.pair_streams * sp.pair_rows + (size_t)2 * sp.streams * sp.single_rows;
+  sp.ml = align_up(rows * c.D * 4, 256);
+  sp.cuts = sp.ml + align_up(rows * 8, 256);
+  sp.total = sp.cuts + align_up((sp.pair_streams + sp.streams) * sizeof(ChunkCut), 256);
+  return sp;
+}
+
+size_t chunk_workspace(const medusa_cfg& c, int T) { return c.dtype == MEDUSA_F32 ? 0 : chunk_space(c, T).total; }
 
 cudaError_t launch_chunk_attention(const medusa_cfg& c, const void* Q, const void* Kp, const void* Vp, void* O, const ChunkArgs& a,
-                                   void*, cudaStream_t st) {
+                                   void* ws, cudaStream_t st) {
   if (c.dtype == MEDUSA_F32) return c.D == 64 ? run<float, 64>(Q, Kp, Vp, O, a, st) : run<float, 128>(Q, Kp, Vp, O, a, st);
-  return c.D == 64 ? run<uint16_t, 64>(Q, Kp, Vp, O, a, st) : run<uint16_t, 128>(Q, Kp, Vp, O, a, st);
+  const ChunkSpace sp = chunk_space(c, a.T);
+  const cudaError_t e = launch_chunk_tc(c, Q, Kp, Vp, O, a, sp, ws, st);
+  if (e != cudaSuccess) return e;
+  return c.D == 64 ? merge<uint16_t, 64>(c, O, sp, ws, st) : merge<uint16_t, 128>(c, O, sp, ws, st);
 }
 
 }  // namespace medusa

@@ -39,6 +39,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "chunk.cuh"
 #include "common.cuh"
 #include "prompt_walk.cuh"
 #include "tc_common.cuh"
@@ -84,12 +85,18 @@ struct RowsArgs {
   int units_s, splits_s, chunk_s, dual_s;   // units, key ranges and their length of the shared rows; 1: dual units
   int units_u, splits_u, dual_u;            // the same of the sequences' own rows (a length for each sequence)
   float scale_log2;
-  uint16_t* O;             // prompts
-  float* o_part;           // prefix: [split][row][D], row = position * Hq + head
+  uint16_t* O;             // prompts, chunks
+  float* o_part;           // prefix: [split][row][D], row = position * Hq + head; chunks: as ChunkSpace counts rows
   float* ml_part;          // prefix: [split][row][2]
+  const int32_t* start;    // chunks: [B] or NULL
+  int window, sinks;       // chunks
+  ChunkSpace space;        // chunks
+  ChunkCut* cuts;          // chunks: of the streams of pairs, then of single tiles
 };
 
-enum UnitKind : int { kEnd = 0, kPrompt = 1, kShared = 2, kOwn = 3 };
+// What the rows are: whole prompts, trees behind a shared prefix, or new tokens over a paged cache.
+enum Mode : int { kPromptMode = 0, kPrefixMode = 1, kChunkMode = 2 };
+enum UnitKind : int { kEnd = 0, kPrompt = 1, kShared = 2, kOwn = 3, kNew = 4 };
 
 // What the scheduling warp hands to the others. Where the rows of a key range fill one tile only
 // (prefix), the two tiles are two such pieces of work, so that there is still one tile's softmax
@@ -101,7 +108,11 @@ struct Unit {
   int base[2];            // prompts: packed row of the sequence's row 0; prefix: the sequence
   int k0[2], kend[2];     // key range
   int n[2], tree[2];      // key tiles (the tree tile included); number of the tree tile, or -1
-  int part[2];            // prefix: which partial result the tile writes
+  int part[2];            // prefix: which partial result the tile writes; chunks: its first row there, or -1 (none: O)
+  // chunks: each half is written by a warp of its own
+  int more[2];            // 0: that warp has come to its end
+  int p0[2];              // logical row of the tile's first row
+  int j0[2], skip[2];     // the part's first tile among the unit's, and what they skip behind the first rows
 };
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -284,15 +295,85 @@ __device__ __forceinline__ Piece decode_prefix(const RowsArgs& a, int u, int t) 
   return w;
 }
 
-template <int kD, bool kPrefix>
+// The units of new tokens over a paged cache that fall into this CTA's ranges: tile t of each, by a
+// warp for each t. Pairs come first, with both tiles over the same keys (both warps go through the same
+// ones); then single tiles, a stream of them for each t.
+struct ChunkFeed {
+  ChunkWalk<7> walk;
+  int64_t x, end, range;
+  int off, phase, stream;   // phase 0: pairs, 1: singles, 2: done
+
+  __device__ __forceinline__ void open(const RowsArgs& a, int t) {
+    const ChunkSpace& sp = a.space;
+    for (; phase < 2; ++phase) {
+      const int streams = phase == 0 ? sp.pair_streams : sp.streams;
+      if (streams == 0) continue;
+      const int log_npos = 31 - __clz(sp.npos);
+      if (phase == 0) walk.choose(log_npos + 1, sp.npos + 1, INT32_MAX);
+      else walk.choose(log_npos, 1, sp.npos);
+      stream = phase == 0 ? (int)blockIdx.x : t * kSms + (int)blockIdx.x;
+      const int64_t all = walk.total();
+      range = max((int64_t)1, (all + streams - 1) / streams);
+      x = min(all, stream * range);
+      end = min(all, x + range);
+      if ((threadIdx.x & 31) == 0 && (phase == 1 || t == 0))
+        a.cuts[phase == 0 ? stream : sp.pair_streams + stream] = ChunkCut{0, 0, 0, 0};
+      if (x < end) {
+        off = walk.seek(x);
+        return;
+      }
+    }
+  }
+  // This warp's half of the next unit; false: there is none.
+  __device__ __forceinline__ bool next(const RowsArgs& a, int t, Unit& d) {
+    if (phase == 2) return false;
+    const ChunkSpace& sp = a.space;
+    const int lane = threadIdx.x & 31, npos = sp.npos;
+    const int all = walk.count(), n = (int)min((int64_t)(all - off), end - x);
+    const int row0 = walk.first_row() + (phase == 0 ? t * npos : 0), left = walk.n - row0;
+    const int p_first = walk.s + walk.first_row(), skip = walk.tiles.skip(p_first);
+    const int upto = left > 0 ? ((walk.s + min(walk.n, row0 + npos) - 1) >> 7) + 1 - skip : 0;   // the tile's own tiles
+    const bool cut = off > 0 || n < all;   // (a unit that is cut writes partial results)
+    if (lane == 0) {
+      d.more[t] = 1;
+      d.dual = phase;
+      d.pos0[t] = walk.c0 + row0;
+      d.left[t] = left;
+      d.h0[t] = walk.hg << a.gp_shift;
+      d.kvh[t] = (walk.hg << a.gp_shift) / (a.Hq / a.Hkv);
+      d.base[t] = walk.b;
+      d.kend[t] = left > 0 ? walk.s + min(walk.n, row0 + npos) : 0;
+      d.n[t] = max(0, min(n, upto - off));
+      d.part[t] = !cut ? -1 : (int)(phase == 0 ? sp.pair_part(stream, off == 0) + t * kRows : sp.single_part(stream, off == 0));
+      d.p0[t] = walk.s + row0;
+      d.j0[t] = off;
+      d.skip[t] = skip;
+      if (cut && off == 0 && (phase == 1 || t == 0))
+        a.cuts[phase == 0 ? stream : sp.pair_streams + stream] =
+            ChunkCut{walk.c0 + walk.first_row(), walk.n - walk.first_row(), walk.hg << a.gp_shift, (int)((x + all - 1) / range) - stream};
+    }
+    x += n;
+    off = 0;
+    if (x < end) {
+      walk.next();
+    } else {
+      ++phase;
+      open(a, t);
+    }
+    return true;
+  }
+};
+
+template <int kD, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKt,
                const __grid_constant__ CUtensorMap tmVt, const __grid_constant__ RowsArgs a) {
   using Lay = Layout<kD>;
   constexpr int kStages = Lay::stages, kTile = Lay::tile, kHalves = Lay::halves;
+  constexpr bool kPrefix = kMode == kPrefixMode, kChunk = kMode == kChunkMode;
   // (Behind a prefix the next kernel's blocks, started early, would crowd the SMs that are done first.)
-  if (!kPrefix) pdl_trigger();
+  if (kMode == kPromptMode) pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = sm + Lay::ring;
@@ -317,7 +398,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       tc::mbar_init(&p_half[t], kRows);
       tc::mbar_init(&p_full[t], kRows);
       tc::mbar_init(&o_done[t], 1);
-      tc::mbar_init(&unit_full[t], 1);
+      tc::mbar_init(&unit_full[t], kChunk ? 2 : 1);
       tc::mbar_init(&unit_empty[t], 10);   // 8 softmax warps, the MMA warp, the load warp
     }
     tc::mbar_init(&tail, 1);
@@ -340,10 +421,44 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     w = units[i & 1];
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&unit_empty[i & 1]);
-    return w.kind != kEnd;
+    return kChunk ? (w.more[0] | w.more[1]) != 0 : w.kind != kEnd;
   };
 
-  if (warp == kPlanWarp) {
+  if (kChunk && warp >= kPlanWarp) {
+    // ------------------------------------------------------------------ schedule: ranges of the work
+    const int t = warp - kPlanWarp;
+    ChunkFeed feed;
+    feed.phase = 0;
+    {
+      ChunkArgs c{};
+      c.cu = a.cu;
+      c.start = a.start;
+      c.B = a.B;
+      c.T = a.T;
+      c.L_cap = a.L_cap;
+      c.Hq = a.Hq;
+      c.window = a.window;
+      c.sinks = a.sinks;
+      feed.walk.begin(c, a.gp_shift);
+    }
+    feed.open(a, t);
+    for (int i = 0;; ++i) {
+      if (i >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&unit_empty[i & 1], ((i >> 1) - 1) & 1, err, 2))) break;
+      Unit& d = units[i & 1];
+      if (!feed.next(a, t, d) && lane == 0) {   // (the other tile may still have some)
+        d.more[t] = d.n[t] = d.left[t] = 0;
+        d.dual = 1;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&unit_full[i & 1]);
+      __syncwarp();
+      // both halves are there: the end is where neither has a unit
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(&unit_full[i & 1], (i >> 1) & 1, err, 1))) break;
+      const bool more = d.more[0] | d.more[1];
+      __syncwarp();
+      if (!more) break;
+    }
+  } else if (warp == kPlanWarp) {
     // ------------------------------------------------------------------ schedule
     // Block indices are units in order. The CTA begins with its own and then takes over blocks
     // that have not started, so that the SMs run out of work together.
@@ -405,21 +520,25 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     Unit w;
     int it = 0, nq[2] = {0, 0}, fixes = 0;   // ring position, Q tiles loaded, tails zeroed
     int page_reg[2] = {-1, -1};
+    ChunkTiles<7> list;
+    list.window = a.window;
+    list.sink_tiles = (int)(((unsigned)a.sinks + (kKeys - 1)) / kKeys);
     int seen = -1;   // prefix: shared rows that any sequence sees (once it is known: rows past it may hold anything)
     bool ok = true;
     for (int i = 0; ok && next_unit(i, w); ++i) {
       const int nt = max(w.n[0], w.n[1]), tiles = w.dual ? 2 : 1;
-      if (nt <= kAhead && lane == 0) tc::mbar_arrive(&want);   // time to fetch the next unit
+      if (!kChunk && nt <= kAhead && lane == 0) tc::mbar_arrive(&want);   // time to fetch the next unit
 #pragma unroll 1
       for (int j = nt > 0 ? -1 : 0; ok && j < nt; ++j) {   // step j: V_j and K_{j+1}
-        if (j > 0 && nt - j == kAhead && lane == 0) tc::mbar_arrive(&want);
+        if (!kChunk && j > 0 && nt - j == kAhead && lane == 0) tc::mbar_arrive(&want);
 #pragma unroll 1
         for (int x = 0; ok && x < 2 * tiles; ++x) {
           const int t = x >> 1, n = w.dual ? (t ? w.n[1] : w.n[0]) : nt, jt = j + (x & 1);
           const bool isv = !(x & 1);
           if (jt < 0 || jt >= n) continue;
           // a tile's rows go ahead of its first K tile; tile 1's, where both share the keys, behind it
-          const int r = j < 0 ? t : (j == 0 && x == 0 && !w.dual && w.n[1] > 0) ? 1 : -1;
+          // (a part of a pair may have none of tile 0's keys)
+          const int r = j < 0 ? (kChunk && w.n[0] == 0 ? (w.dual ? t : -1) : t) : (j == 0 && x == 0 && !w.dual && w.n[1] > 0) ? 1 : -1;
           if (r >= 0) {
             const int used = r ? nq[1] : nq[0];
             if (used > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty[r], (used - 1) & 1, err, 4));
@@ -440,9 +559,10 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           if (it >= kStages) ok = __all_sync(0xffffffffu, tc::mbar_wait<true>(&kv_empty[st], (it / kStages - 1) & 1, err, 8));
           if (!ok) break;
           const bool tree = kPrefix && jt == (t ? w.tree[1] : w.tree[0]);
-          const int key0 = k0 + jt * kKeys;
+          const int skip = t ? w.skip[1] : w.skip[0], j0 = t ? w.j0[1] : w.j0[0];
+          const int key0 = kChunk ? list.tile(j0 + jt, skip) * kKeys : k0 + jt * kKeys;
           int y, z;
-          if (!kPrefix) {
+          if (kMode == kPromptMode) {
             y = base + key0;
             z = kvh;
           } else if (tree) {
@@ -451,10 +571,10 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           } else {
             int pages = t ? page_reg[1] : page_reg[0];
             if (!isv && (jt & 31) == 0) {   // 32 tiles' pages at a time, one per lane
-              const int key = key0 + lane * kKeys;
+              const int key = kChunk ? list.tile(j0 + jt + lane, skip) * kKeys : key0 + lane * kKeys;
               pages = -1;
-              if (key < kend)
-                pages = w.kind == kShared ? a.prefix[key / a.page_rows] : a.table[(size_t)base * a.max_pages + key / a.page_rows];
+              if (kChunk ? jt + lane < n : key < kend)
+                pages = !kChunk && w.kind == kShared ? a.prefix[key / a.page_rows] : a.table[(size_t)base * a.max_pages + key / a.page_rows];
               if (t) page_reg[1] = pages;
               else page_reg[0] = pages;
             }
@@ -476,7 +596,11 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           }
           const int last = kPrefix && w.kind == kShared ? min(kend, seen) : kend;
           const int live = tree ? kKeys : max(0, min(kKeys, last - key0));   // (rows past the tree's nodes arrive as zeros)
-          const bool fix = isv && live < kKeys;
+          // chunks: what no row of the unit sees (a part's tiles are of a pair: tile 0's first row, tile 1's last)
+          const int low = kChunk ? max(0, (t ? w.p0[1] : w.p0[0]) - a.window + 1) - key0 : 0;
+          const int high = kChunk ? min(kKeys, (w.dual ? kend : max(w.kend[0], w.kend[1])) - key0) : live;
+          const int first = kChunk ? a.sinks - key0 : 0;   // rows below it stay visible
+          const bool fix = isv && (high < kKeys || (kChunk && low > 0 && first < min(low, kKeys)));
           uint64_t* bar = fix ? &tail : &kv_full[st];
           if (lane == 0) {
             tc::mbar_arrive_expect(bar, kTile);
@@ -489,7 +613,8 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             ++fixes;
             if (!ok) break;
 #pragma unroll 1
-            for (int c = live * 8 + lane; c < kKeys * 8; c += 32) {
+            for (int c = (kChunk ? 0 : live * 8) + lane; c < kKeys * 8; c += 32) {
+              if (kChunk && (c >> 3) < high && ((c >> 3) >= low || (c >> 3) < first)) continue;
 #pragma unroll
               for (int h = 0; h < kHalves; ++h) reinterpret_cast<uint4*>(dst + h * kHalf)[c] = make_uint4(0, 0, 0, 0);
             }
@@ -614,7 +739,9 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             // 1's last, if everything for it is there.
             if (ok && t == 0 && !dual && j + 1 == nt && mbar_test(&unit_full[(i + 1) & 1], ((i + 1) >> 1) & 1)) {
               const int n0 = units[(i + 1) & 1].n[0];
-              if (units[(i + 1) & 1].kind != kEnd && n0 > 0 && mbar_test(&kv_full[st], ph) && mbar_test(&q_full[0], nq[0] & 1)) {
+              const bool on = kChunk ? (units[(i + 1) & 1].more[0] | units[(i + 1) & 1].more[1]) != 0 && !units[(i + 1) & 1].dual
+                                     : units[(i + 1) & 1].kind != kEnd;
+              if (on && n0 > 0 && mbar_test(&kv_full[st], ph) && mbar_test(&q_full[0], nq[0] & 1)) {
                 tc::fence_after();
                 ++nq[0];
                 issue_S(0, st);
@@ -632,12 +759,13 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       for (int i = 0; ok; ++i) {
         ok = tc::mbar_wait(&unit_full[i & 1], (i >> 1) & 1, err, 1);
         if (!ok) break;
-        const bool end = units[i & 1].kind == kEnd, two = units[i & 1].dual;
+        const bool end = kChunk ? !(units[i & 1].more[0] | units[i & 1].more[1]) : units[i & 1].kind == kEnd;
+        const bool two = units[i & 1].dual;
         const int n[2] = {units[i & 1].n[0], units[i & 1].n[1]};
         tc::mbar_arrive(&unit_empty[i & 1]);
         if (end) break;
         if (max(n[0], n[1]) == 0) continue;
-        if (kPrefix && two) issue_unit(std::true_type{}, i, n);
+        if (kMode != kPromptMode && two) issue_unit(std::true_type{}, i, n);
         else issue_unit(std::false_type{}, i, n);
       }
     }
@@ -648,6 +776,9 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + col_S(t) + lanes, tO = tmem + col_O(t) + lanes;
     const int rhead = row >> (7 - a.gp_shift), rpos = row & (npos - 1);
+    ChunkTiles<7> list;
+    list.window = a.window;
+    list.sink_tiles = (int)(((unsigned)a.sinks + (kKeys - 1)) / kKeys);
     int ns = 0, nu = 0;   // S tiles and units taken
     bool ok = true;
     for (int i = 0; ok; ++i) {
@@ -656,14 +787,20 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       const Unit& w = units[i & 1];
       const int kind = w.kind, n = w.n[t], k0 = w.k0[t], kend = w.kend[t], tree_tile = w.tree[t], left = w.left[t];
       const int pos = w.pos0[t] + rpos, head = w.h0[t] + rhead, base = w.base[t], part_no = w.part[t];
+      const bool end = kChunk ? !(w.more[0] | w.more[1]) : kind == kEnd;
+      const int p = w.p0[t] + rpos, j0 = w.j0[t], skip = w.skip[t], single = w.dual;   // chunks
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&unit_empty[i & 1]);
-      if (kind == kEnd) break;
+      if (end) break;
       const bool row_ok = rpos < left;
       // keys below `limit` are visible to this row
       int limit = kend;
       uint64_t word0 = 0, word1 = 0;
-      if (!kPrefix) {
+      int low = 0;   // chunks: and those from `low` on, or below a.sinks
+      if (kChunk) {
+        limit = p + 1;
+        low = max(0, p - a.window + 1);
+      } else if (!kPrefix) {
         limit = pos - base + 1;
       } else if (row_ok) {
         const int b = pos / a.N;
@@ -688,14 +825,19 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + 32 * c, v + 32 * c);
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_landed32(v + 32 * c);
-          const int vis = limit - (k0 + j * kKeys);
-          const bool tree = kPrefix && j == tree_tile, masked = tree || __any_sync(0xffffffffu, vis < kKeys);
+          const int key0 = kChunk ? list.tile(j0 + j, skip) * kKeys : k0 + j * kKeys;
+          const int vis = limit - key0;
+          const bool tree = kPrefix && j == tree_tile;
+          const bool masked = kChunk ? __any_sync(0xffffffffu, row_ok && (vis < kKeys || (low > key0 && a.sinks - key0 < min(low - key0, kKeys))))
+                                     : tree || __any_sync(0xffffffffu, vis < kKeys);
           if (masked) {   // a bit per key, so that one piece of code masks the tree's tiles and the others
             uint32_t see[4] = {(uint32_t)word0, (uint32_t)(word0 >> 32), (uint32_t)word1, (uint32_t)(word1 >> 32)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int here = vis - 32 * c;
-              if (!tree) see[c] = here >= 32 ? 0xffffffffu : here <= 0 ? 0u : (1u << here) - 1u;
+              auto below = [](int x) { return x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1u; };
+              if (!tree) see[c] = below(here);
+              if (kChunk) see[c] &= ~below(low - key0 - 32 * c) | below(a.sinks - key0 - 32 * c);
 #pragma unroll
               for (int x = 0; x < 32; ++x)
                 v[32 * c + x] = (see[c] >> x) & 1u ? v[32 * c + x] : __float_as_uint(-INFINITY);
@@ -705,7 +847,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           float corr = 1.f;
           uint32_t pk[16];
           const float m_tile = fmaxf(fmaxf(max32(v), max32(v + 32)), fmaxf(max32(v + 64), max32(v + 96))) * a.scale_log2;
-          const bool move = m_tile > m_run + kLazy;   // also on the first visible tile (m_run = -inf): corr = 0
+          const bool move = m_tile > m_run + kLazy && (!kChunk || row_ok);   // also on the first visible tile (m_run = -inf): corr = 0
           if (__any_sync(0xffffffffu, move)) {
             if (move) {
               corr = tc::ex2(m_run - m_tile);
@@ -762,7 +904,8 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       const int quad = lane & 3;
       const size_t orow = (size_t)pos * a.Hq + head, orow0 = (size_t)(pos - quad) * a.Hq + head;
       const int rows_here = left - (rpos - quad);   // rows of the four that exist, if positive
-      if (!kPrefix) {
+      const bool direct = kMode == kPromptMode || (kChunk && part_no < 0);
+      if (direct) {
         const float inv = 1.f / l_run;   // (0 where every visible score is -inf: 0 times inf, no number, as in float32)
 #pragma unroll 1
         for (int c = 0; c < kD / 32; ++c) {
@@ -780,7 +923,11 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
               *reinterpret_cast<uint4*>(op + (size_t)k * a.Hq * kD) = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
         }
       } else {
-        const size_t part = (size_t)part_no * a.T * a.Hq;
+        // chunks: rows in the tile's order, [head][position]
+        const int along = single ? a.space.single_npos : npos;
+        const size_t part = kChunk ? (size_t)part_no + (size_t)rhead * along : (size_t)part_no * a.T * a.Hq;
+        const size_t at0 = kChunk ? part + rpos - quad : part + orow0, at = kChunk ? part + rpos : part + orow;
+        const size_t step = kChunk ? 1 : a.Hq;
         if (n > 0) {
 #pragma unroll 1
           for (int c = 0; c < kD / 32; ++c) {
@@ -790,18 +937,18 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               transpose4(o + 16 * x);
-              float* op = a.o_part + (part + orow0) * kD + 32 * c + 16 * x + 4 * quad;
+              float* op = a.o_part + at0 * kD + 32 * c + 16 * x + 4 * quad;
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 if (k < rows_here)
-                  *reinterpret_cast<uint4*>(op + (size_t)k * a.Hq * kD) =
+                  *reinterpret_cast<uint4*>(op + k * step * kD) =
                       make_uint4(o[16 * x + 4 * k], o[16 * x + 4 * k + 1], o[16 * x + 4 * k + 2], o[16 * x + 4 * k + 3]);
             }
           }
         }
         if (row_ok) {
-          a.ml_part[2 * (part + orow)] = m_run;
-          a.ml_part[2 * (part + orow) + 1] = l_run;
+          a.ml_part[2 * at] = m_run;
+          a.ml_part[2 * at + 1] = l_run;
         }
       }
       tc::fence_before();   // O has been read before the next unit's first P is announced
@@ -1128,11 +1275,11 @@ PrefixPlan plan_prefix(const medusa_cfg& c, int shared) {
   return p;
 }
 
-template <int D, bool kPrefix>
+template <int D, int kMode>
 cudaError_t launch_rows(const CUtensorMap* m, const RowsArgs& a, int64_t units, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<D, kPrefix>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::smem);
+  cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<D, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(rows_tc_kernel<D, kPrefix>, (unsigned)units, kThreads, Layout<D>::smem, st, m[0], m[1], m[2], m[3],
+  e = launch_pdl(rows_tc_kernel<D, kMode>, (unsigned)units, kThreads, Layout<D>::smem, st, m[0], m[1], m[2], m[3],
                  m[4], a);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -1169,7 +1316,7 @@ cudaError_t launch_prompt_tc(const medusa_cfg& c, const void* Q, const void* K, 
   m[3] = m[1];
   m[4] = m[2];
   const int64_t units = ((int64_t)T / (2 * npos) + c.B) * (c.Hq >> a.gp_shift);   // at least as many as there are
-  return c.D == 64 ? launch_rows<64, false>(m, a, units, st) : launch_rows<128, false>(m, a, units, st);
+  return c.D == 64 ? launch_rows<64, kPromptMode>(m, a, units, st) : launch_rows<128, kPromptMode>(m, a, units, st);
 }
 
 size_t prefix_workspace(const medusa_cfg& c, int shared) { return plan_prefix(c, shared).total; }
@@ -1216,7 +1363,7 @@ cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const vo
       !encode_3d(&m[4], kPrefixD, Vt, ts.N, tplanes, kPrefixD * 2, (uint64_t)ts.N * kPrefixD * 2, kKeys, 1))
     return cudaErrorInvalidValue;
   if (p.units_s + p.units_u > 0) {
-    const cudaError_t e = launch_rows<kPrefixD, true>(m, a, p.units_s + p.units_u, st);
+    const cudaError_t e = launch_rows<kPrefixD, kPrefixMode>(m, a, p.units_s + p.units_u, st);
     if (e != cudaSuccess) return e;
   }
   cudaError_t e;
@@ -1233,6 +1380,41 @@ cudaError_t launch_prefix_attention(const medusa_cfg& c, const void* Q, const vo
                  static_cast<const float*>(a.ml_part), rows, p.parts, static_cast<uint16_t*>(O));
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// One CTA per SM; what each does comes from its ranges of the work.
+cudaError_t launch_chunk_tc(const medusa_cfg& c, const void* Q, const void* Kp, const void* Vp, void* O, const ChunkArgs& ca,
+                            const ChunkSpace& sp, void* ws, cudaStream_t st) {
+  RowsArgs a{};
+  a.cu = ca.cu;
+  a.start = ca.start;
+  a.table = ca.table;
+  a.B = ca.B;
+  a.T = ca.T;
+  a.Hq = ca.Hq;
+  a.Hkv = ca.Hkv;
+  a.gp_shift = sp.gp_shift;
+  a.L_cap = ca.L_cap;
+  a.page_rows = ca.page_rows;
+  a.max_pages = ca.max_pages;
+  a.num_pages = ca.num_pages;
+  a.window = ca.window;
+  a.sinks = ca.sinks;
+  a.scale_log2 = ca.scale_log2;
+  a.O = static_cast<uint16_t*>(O);
+  a.space = sp;
+  a.o_part = static_cast<float*>(ws);
+  a.ml_part = reinterpret_cast<float*>(static_cast<char*>(ws) + sp.ml);
+  a.cuts = reinterpret_cast<ChunkCut*>(static_cast<char*>(ws) + sp.cuts);
+  const uint64_t planes = (uint64_t)ca.num_pages * c.Hkv;
+  CUtensorMap m[5];
+  if (!encode_3d(&m[0], c.D, Q, ca.T, c.Hq, ca.q_stride * 2, c.D * 2, sp.npos, 1u << sp.gp_shift) ||
+      !encode_3d(&m[1], c.D, Kp, ca.page_rows, planes, c.D * 2, (uint64_t)ca.page_rows * c.D * 2, kKeys, 1) ||
+      !encode_3d(&m[2], c.D, Vp, ca.page_rows, planes, c.D * 2, (uint64_t)ca.page_rows * c.D * 2, kKeys, 1))
+    return cudaErrorInvalidValue;
+  m[3] = m[1];
+  m[4] = m[2];
+  return c.D == 64 ? launch_rows<64, kChunkMode>(m, a, kSms, st) : launch_rows<128, kChunkMode>(m, a, kSms, st);
 }
 
 }  // namespace medusa
