@@ -112,7 +112,8 @@ int chunk_attention(const medusa_cfg* cfg, const void* Q, int T, int64_t q_strid
     return MEDUSA_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(Kp) || !aligned16(Vp) || !aligned16(O) || !aligned256(workspace)) return MEDUSA_ERR_INVALID_ARG;
   if (!row_stride_ok(*cfg, q_stride, cfg->Hq)) return MEDUSA_ERR_INVALID_ARG;
-  if (((int64_t)num_pages + 1) * cfg->Hkv > INT32_MAX) return MEDUSA_ERR_UNSUPPORTED;   // page planes are counted in 32 bits
+  // page planes and key tiles are counted in 32 bits
+  if (((int64_t)num_pages + 1) * cfg->Hkv > INT32_MAX || !chunk_countable(*cfg, T)) return MEDUSA_ERR_UNSUPPORTED;
   ChunkArgs a{};
   a.cu = cu_rows;
   a.start = start;

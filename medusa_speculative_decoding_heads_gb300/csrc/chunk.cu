@@ -71,8 +71,8 @@ cudaError_t run(const void* Q, const void* Kp, const void* Vp, void* O, const Ch
 }
 
 // Joins the partial results of the units that were cut: O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s, a warp
-// per row, kMergeRows rows of a unit per CTA. Bound by the partial results' bytes, which lie in L2.
-constexpr int kMergeThreads = 256, kMergeRows = 32;
+// per row, several parts on their way at a time. Bound by the partial results' bytes, which lie in L2.
+constexpr int kMergeThreads = 256, kMergeRows = kMergeThreads / 32, kMergeParts = 4;
 
 template <int X>
 struct Vec;
@@ -89,52 +89,62 @@ chunk_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m
   using V = typename Vec<X>::type;
   pdl_wait();
   pdl_trigger();
-  const bool pair = (int)blockIdx.x < sp.pair_streams;
-  const int stream = pair ? (int)blockIdx.x : (int)blockIdx.x - sp.pair_streams;
-  const ChunkCut cut = cuts[blockIdx.x];
-  if (cut.parts == 0) return;
-  const int rows = pair ? sp.pair_rows : sp.single_rows, along = pair ? sp.npos : sp.single_npos, lane = threadIdx.x & 31;
-  const int tile_rows = along << sp.gp_shift;
-  for (int r = blockIdx.y * kMergeRows + (threadIdx.x >> 5); r < min(rows, (int)(blockIdx.y + 1) * kMergeRows); r += kMergeThreads / 32) {
-    const int tile = r / tile_rows, head = (r - tile * tile_rows) / along, pos = r - tile * tile_rows - head * along + tile * along;
-    if (pos >= cut.left) continue;
-    float M = -INFINITY, sum = 0.f, acc[X] = {};
-    for (int s = 0; s <= cut.parts; ++s) {
+  // blocks: kMergeRows rows of each stream of pairs, then of single tiles
+  const int per_pair = sp.pair_rows / kMergeRows, per_single = (sp.single_rows + kMergeRows - 1) / kMergeRows;
+  const bool pair = (int)blockIdx.x < sp.pair_streams * per_pair;
+  const int y = pair ? (int)blockIdx.x : (int)blockIdx.x - sp.pair_streams * per_pair;
+  const int stream = y / (pair ? per_pair : per_single), lane = threadIdx.x & 31;
+  const int r = (y - stream * (pair ? per_pair : per_single)) * kMergeRows + (threadIdx.x >> 5);
+  const ChunkCut cut = cuts[(pair ? 0 : sp.pair_streams) + stream];
+  if (cut.parts == 0 || r >= (pair ? sp.pair_rows : sp.single_rows)) return;
+  const int along = pair ? sp.npos : sp.single_npos, tile_rows = along << sp.gp_shift;   // rows of a tile: [head][position]
+  const int tile = r / tile_rows, head = (r - tile * tile_rows) / along, pos = r - tile * tile_rows - head * along + tile * along;
+  if (pos >= cut.left) return;
+  float M = -INFINITY, sum = 0.f, acc[X] = {};
+  for (int s0 = 0; s0 <= cut.parts; s0 += kMergeParts) {
+    float2 ml[kMergeParts];
+    V v[kMergeParts];
+#pragma unroll
+    for (int i = 0; i < kMergeParts; ++i) {
+      const int s = min(s0 + i, cut.parts);
       const int64_t at = (pair ? sp.pair_part(stream + s, s == 0) : sp.single_part(stream + s, s == 0)) + r;
-      const float2 ml = *reinterpret_cast<const float2*>(ml_part + 2 * at);
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;   // nothing was visible: its O need not have been written
-      const V v = *reinterpret_cast<const V*>(o_part + at * D + X * lane);
-      const float* o = reinterpret_cast<const float*>(&v);
-      const float mn = fmaxf(M, ml.x), mu = mn == -INFINITY ? 0.f : mn, w0 = exp2f(M - mu), w1 = exp2f(ml.x - mu);
+      ml[i] = *reinterpret_cast<const float2*>(ml_part + 2 * at);
+      v[i] = *reinterpret_cast<const V*>(o_part + at * D + X * lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeParts; ++i) {
+      // (where nothing was visible its O need not have been written)
+      if (s0 + i > cut.parts || (ml[i].x == -INFINITY && ml[i].y == 0.f)) continue;
+      const float* o = reinterpret_cast<const float*>(&v[i]);
+      const float mn = fmaxf(M, ml[i].x), mu = mn == -INFINITY ? 0.f : mn, w0 = exp2f(M - mu), w1 = exp2f(ml[i].x - mu);
       M = mn;
-      sum = sum * w0 + ml.y * w1;
+      sum = sum * w0 + ml[i].y * w1;
 #pragma unroll
       for (int x = 0; x < X; ++x) acc[x] = acc[x] * w0 + o[x] * w1;
     }
-    const float inv = 1.f / sum;   // (0 where every visible score is -inf: no number)
-    T* op = O + ((size_t)(cut.pos0 + pos) * Hq + cut.h0 + head) * D + X * lane;
-    if constexpr (sizeof(T) == 4) {
-      V v;
+  }
+  const float inv = 1.f / sum;   // (0 where every visible score is -inf: no number)
+  T* op = O + ((size_t)(cut.pos0 + pos) * Hq + cut.h0 + head) * D + X * lane;
+  if constexpr (sizeof(T) == 4) {
+    V v;
 #pragma unroll
-      for (int x = 0; x < X; ++x) reinterpret_cast<float*>(&v)[x] = acc[x] * inv;
-      *reinterpret_cast<V*>(op) = v;
-    } else {
+    for (int x = 0; x < X; ++x) reinterpret_cast<float*>(&v)[x] = acc[x] * inv;
+    *reinterpret_cast<V*>(op) = v;
+  } else {
 #pragma unroll
-      for (int x = 0; x < X; x += 2) {
-        uint32_t w;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(acc[x + 1] * inv), "f"(acc[x] * inv));
-        reinterpret_cast<uint32_t*>(op)[x / 2] = w;
-      }
+    for (int x = 0; x < X; x += 2) {
+      uint32_t w;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(acc[x + 1] * inv), "f"(acc[x] * inv));
+      reinterpret_cast<uint32_t*>(op)[x / 2] = w;
     }
   }
 }
 
 template <typename T, int D>
 cudaError_t merge(const medusa_cfg& c, void* O, const ChunkSpace& sp, void* ws, cudaStream_t st) {
-  const int rows = sp.pair_streams ? sp.pair_rows : sp.single_rows;
-  const dim3 grid(sp.pair_streams + sp.streams, (rows + kMergeRows - 1) / kMergeRows);
+  const int blocks = sp.pair_streams * (sp.pair_rows / kMergeRows) + sp.streams * ((sp.single_rows + kMergeRows - 1) / kMergeRows);
   const char* base = static_cast<const char*>(ws);
-  const cudaError_t e = launch_pdl(chunk_merge_kernel<T, D>, grid, kMergeThreads, 0, st, reinterpret_cast<const float*>(base),
+  const cudaError_t e = launch_pdl(chunk_merge_kernel<T, D>, blocks, kMergeThreads, 0, st, reinterpret_cast<const float*>(base),
                                    reinterpret_cast<const float*>(base + sp.ml), reinterpret_cast<const ChunkCut*>(base + sp.cuts), sp,
                                    c.Hq, static_cast<T*>(O));
   note_launches(1);
@@ -153,7 +163,7 @@ ChunkSpace chunk_space(const medusa_cfg& c, int T) {
   sp.npos = kRows >> sp.gp_shift;
   sp.pair_streams = T > sp.npos ? kSms : 0;   // (no sequence has more rows than there are)
   sp.pair_rows = 2 * kRows;
-  sp.streams = 2 * kSms;
+  sp.streams = kSms;
   sp.single_npos = T < sp.npos ? T : sp.npos;
   sp.single_rows = sp.single_npos << sp.gp_shift;
   const size_t rows = (size_t)2 * sp.pair_streams * sp.pair_rows + (size_t)2 * sp.streams * sp.single_rows;
@@ -161,6 +171,12 @@ ChunkSpace chunk_space(const medusa_cfg& c, int T) {
   sp.cuts = sp.ml + align_up(rows * 8, 256);
   sp.total = sp.cuts + align_up((sp.pair_streams + sp.streams) * sizeof(ChunkCut), 256);
   return sp;
+}
+
+bool chunk_countable(const medusa_cfg& c, int T) {
+  const ChunkSpace sp = chunk_space(c, T);
+  const double units = ((double)T / sp.npos + c.B) * (c.Hq >> sp.gp_shift);
+  return units * (c.L_cap / 128 + 4.0) < 2147483647.0;   // (4: the tile that is begun, what a unit counts for beside)
 }
 
 size_t chunk_workspace(const medusa_cfg& c, int T) { return c.dtype == MEDUSA_F32 ? 0 : chunk_space(c, T).total; }

@@ -3,11 +3,10 @@
 // Work. A unit is a block of query rows (the query heads of one KV head that share a tile, times
 // positions) of one sequence; it takes the key tiles that any of its rows sees, the first rows' ones
 // ahead of the window's. All units' tiles, one after another, are cut into equal ranges, one for each
-// stream (a CTA, or one of a CTA's two tiles of rows), wherever the cuts fall: lengths differ from
+// stream (a CTA), wherever the cuts fall: lengths differ from
 // sequence to sequence and are on the device only, and so are the cuts. A unit that is cut leaves partial
 // results, at most two per stream (of the unit that was begun ahead of its range, and of the one that
-// ends behind it), which chunk_merge_kernel joins. Where a unit lies among the tiles is known in closed
-// form: rows per unit and keys per tile are powers of two.
+// ends behind it), which chunk_merge_kernel joins.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -51,9 +50,9 @@ struct ChunkSpace {
 template <int kShift>
 struct ChunkTiles {
   int window, sink_tiles;
-  __device__ __forceinline__ void begin(const ChunkArgs& a) {
-    window = a.window;
-    sink_tiles = (int)(((unsigned)a.sinks + ((1u << kShift) - 1)) >> kShift);
+  __device__ __forceinline__ void begin(int window_, int sinks) {
+    window = window_;
+    sink_tiles = (int)(((unsigned)sinks + ((1u << kShift) - 1)) >> kShift);
   }
   // key tiles between the first rows and the window of row p, which nothing of a unit that begins with p sees
   __device__ __forceinline__ int skip(int p) const { return max(0, (max(0, p - window + 1) >> kShift) - sink_tiles); }
@@ -61,159 +60,173 @@ struct ChunkTiles {
   __device__ __forceinline__ int count(int p0, int p1) const { return (p1 >> kShift) + 1 - skip(p0); }
   // key tile that is number j of a unit
   __device__ __forceinline__ int tile(int j, int skipped) const { return j < sink_tiles ? j : j + skipped; }
-
-  // sum over t < m of floor((a + t 2^r) / 2^kShift), a >= 0
-  static __device__ __forceinline__ int64_t floors(int64_t m, int64_t a, int r) {
-    if (r >= kShift) return m * (a >> kShift) + ((m * (m - 1) / 2) << (r - kShift));
-    const int q = kShift - r;
-    auto upto = [&](int64_t k) {   // sum over i < k of floor(i / 2^q)
-      const int64_t j = k >> q;
-      return ((j * (j - 1) / 2) << q) + (k - (j << q)) * j;
-    };
-    return upto((a >> r) + m) - upto(a >> r);
-  }
-  // tiles of the first m of a sequence's units of 2^r rows (n rows from logical row s on)
-  __device__ __forceinline__ int64_t upto(int m, int s, int n, int r) const {
-    const int64_t R = (int64_t)1 << r;
-    int64_t sum = floors(m, s + R - 1, r) + m;
-    const int64_t over = s + m * R;   // one past the last of those units' rows, if it is whole
-    if (over > (int64_t)s + n) sum += ((s + n - 1) >> kShift) - ((over - 1) >> kShift);
-    const int64_t a = (int64_t)s - window + 1 - ((int64_t)sink_tiles << kShift);
-    const int64_t t = a >= 0 ? 0 : (-a + R - 1) >> r;   // the first unit that skips any
-    if (t < m) sum -= floors(m - t, a + t * R, r);
-    return sum;
-  }
 };
 
-// Finds and follows units of one class; a whole warp calls every function.
+// A stream's units of one class, one after another; a whole warp calls every function. (What it does ahead
+// of the first unit is time without any: its code is short, and counted in 32 bits, which the host has checked.)
 template <int kShift>
 struct ChunkWalk {
   ChunkTiles<kShift> tiles;
   const int32_t *cu, *start;
   int B, T, L_cap, HG;
   int r, least, most;   // rows per unit (log2); sequences of least .. most rows
-  // the lanes' sequences, group .. group + 31
-  int group, my_n, my_s, my_c0;
-  // the current unit
-  int b, n, s, c0, t, units, hg;
+  int extra;            // tiles that a unit counts for beside its own, ahead of them: what it costs to go to the next one
+  int x, end, range;    // of all tiles: the next one, one past the stream's last, tiles of a stream
+  int group, my_n, my_s, my_c0, my_w;   // the lanes' sequences group .. group + 31, and their tiles
+  int b, n, s, c0, t, units, hg, off;   // the current unit, and its first tile that is this stream's (extra ones first)
 
   __device__ __forceinline__ int lane() const { return threadIdx.x & 31; }
-  // Sequences from the first decrease of the offsets on have no rows; those that leave [0, T] or the cache neither.
-  __device__ __forceinline__ void load(int g, int& n_, int& s_, int& c0_) const {
-    const int i = g + lane();
-    n_ = s_ = c0_ = 0;
-    if (i >= B) return;
-    const int a = cu[i], e = cu[i + 1], f = start ? start[i] : 0;
-    if (a < 0 || e <= a || e > T || f < 0 || f > L_cap - (e - a)) return;
-    n_ = e - a;
-    s_ = f;
-    c0_ = a;
-  }
-  __device__ __forceinline__ bool in_class(int rows) const { return rows >= least && rows <= most; }
-  __device__ __forceinline__ int64_t work(int n_, int s_) const {
-    return in_class(n_) ? HG * tiles.upto((int)(((int64_t)n_ + (1 << r) - 1) >> r), s_, n_, r) : 0;
-  }
-  static __device__ __forceinline__ int64_t sum(int64_t v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  }
   __device__ __forceinline__ void begin(const ChunkArgs& a, int gp_shift) {
-    tiles.begin(a);
+    tiles.begin(a.window, a.sinks);
     cu = a.cu;
     start = a.start;
     B = a.B;
     T = a.T;
     L_cap = a.L_cap;
     HG = a.Hq >> gp_shift;
-    // (B ends ahead of the first decrease)
-    for (int g = 0; g < B; g += 32) {
-      const int i = g + lane();
-      const unsigned falls = __ballot_sync(0xffffffffu, i < B && cu[i + 1] < cu[i]);
-      if (falls) B = g + __ffs(falls) - 1;
-    }
-    group = 0;
-    load(0, my_n, my_s, my_c0);
+    if (B <= 32) return;
+    // the sequences from the first decrease of the offsets on have no rows
+#pragma unroll 4
+    for (int i = lane(); i < a.B; i += 32)
+      if (cu[i + 1] < cu[i]) B = min(B, i);
+    B = __reduce_min_sync(0xffffffffu, B);
   }
-  __device__ __forceinline__ void choose(int r_, int least_, int most_) {
-    r = r_;
-    least = least_;
-    most = most_;
-  }
-  // Tiles of all units of the class.
-  __device__ int64_t total() {
-    int64_t w = 0;
-    if (B <= 32) return sum(work(my_n, my_s));
-#pragma unroll 2
-    for (int g = 0; g < B; g += 32) {
-      int n_, s_, c_;
-      load(g, n_, s_, c_);
-      w += work(n_, s_);
+  __device__ __forceinline__ bool mine() const { return my_n >= least && my_n <= most; }
+  // The lanes' sequences; those that leave [0, T] or the cache have no rows.
+  __device__ __forceinline__ void load(int g) {
+    const int i = g + lane();
+    group = g;
+    my_n = my_s = my_c0 = 0;
+    int a = 0, e = 0, f = 0;
+    if (i < B) {
+      a = cu[i];
+      e = cu[i + 1];
+      f = start ? start[i] : 0;
     }
-    return sum(w);
+    const unsigned falls = __ballot_sync(0xffffffffu, e < a);
+    if (!(falls & ((2u << lane()) - 1)) && a >= 0 && e > a && e <= T && f >= 0 && f <= L_cap - (e - a)) {
+      my_n = e - a;
+      my_s = f;
+      my_c0 = a;
+    }
+  }
+  __device__ __forceinline__ int units_of(int n_) const { return (int)(((unsigned)n_ + ((1u << r) - 1)) >> r); }
+  // all heads' tiles of units number t_ of n_ rows from logical row s_ on
+  __device__ __forceinline__ int all_heads(int t_, int s_, int n_) const {
+    const int a = t_ << r, e = n_ - a > (1 << r) ? a + (1 << r) : n_;
+    return HG * (tiles.count(s_ + a, s_ + e - 1) + extra);
   }
   __device__ __forceinline__ void take(int from) {   // the sequence of a lane
     b = group + from;
     n = __shfl_sync(0xffffffffu, my_n, from);
     s = __shfl_sync(0xffffffffu, my_s, from);
     c0 = __shfl_sync(0xffffffffu, my_c0, from);
-    units = (int)(((int64_t)n + (1 << r) - 1) >> r);
+    units = units_of(n);
     t = hg = 0;
   }
-  // The unit with tile x of all (x < total()); returns which of its tiles that is.
-  __device__ int seek(int64_t x) {
-    for (group = 0;; group += 32) {
-      if (B > 32) load(group, my_n, my_s, my_c0);
-      const int64_t w = work(my_n, my_s);
-      int64_t upto = w;
+  // Inclusive sums over the lanes.
+  __device__ __forceinline__ int scan(int v) const {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane() >= o) upto += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane() >= o) v += u;
+    }
+    return v;
+  }
+  // The stream's range of the class's tiles and its first unit; false: it has none.
+  __device__ __forceinline__ bool open(int r_, int least_, int most_, int extra_, int stream, int streams) {
+    r = r_;
+    least = least_;
+    most = most_;
+    extra = extra_;
+    int all = 0;
+    x = end = 0;
+    for (int pass = 0;; ++pass) {   // the sum of all; then the sequence with tile x
+      int y = x;
+      for (int g = 0; g < B; g += 32) {
+        if (pass == 0 || B > 32) {
+          load(g);
+          const int m = mine() ? units_of(my_n) : 0;
+          my_w = m == 1 ? all_heads(0, my_s, my_n) : 0;
+          for (unsigned many = __ballot_sync(0xffffffffu, m > 1); many; many &= many - 1) {
+            const int from = __ffs(many) - 1;
+            take(from);
+            int w = 0;
+            for (int i = lane(); i < units; i += 32) w += all_heads(i, s, n);
+            w = __reduce_add_sync(0xffffffffu, w);
+            if (lane() == from) my_w = w;
+          }
+        }
+        const int upto = scan(my_w), sum = __shfl_sync(0xffffffffu, upto, 31);
+        if (pass == 0) {
+          all += sum;
+        } else if (y < sum) {
+          const int from = __ffs(__ballot_sync(0xffffffffu, upto > y)) - 1;
+          y -= __shfl_sync(0xffffffffu, upto - my_w, from);
+          take(from);
+          break;
+        } else {
+          y -= sum;
+        }
       }
-      const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
-      if (x >= all && group + 32 < B) {
-        x -= all;
+      if (pass == 0) {
+        range = max(1, (int)(((unsigned)all + (streams - 1)) / (unsigned)streams));
+        const int64_t first = (int64_t)stream * range;
+        if (first >= all) return false;
+        x = (int)first;
+        end = min(all, x + min(range, all - x));
         continue;
       }
-      const unsigned past = __ballot_sync(0xffffffffu, upto > x);
-      const int from = past ? __ffs(past) - 1 : 31;   // (x < total(): there is one)
-      x -= __shfl_sync(0xffffffffu, upto - w, from);
-      take(from);
-      break;
+      for (; units > 1; t += 32) {   // the unit with that tile
+        const int w = t + lane() < units ? all_heads(t + lane(), s, n) : 0, upto = scan(w);
+        const unsigned past = __ballot_sync(0xffffffffu, upto > y);
+        if (past) {
+          const int from = __ffs(past) - 1;
+          y -= __shfl_sync(0xffffffffu, upto - w, from);
+          t += from;
+          break;
+        }
+        y -= __shfl_sync(0xffffffffu, upto, 31);
+      }
+      const int each = count() + extra;
+      hg = y / each;
+      off = y - hg * each;
+      return true;
     }
-    int lo = 0, hi = units;   // unit lo begins at or ahead of x, unit hi behind it
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) >> 5, at = lo + (lane() + 1) * step;
-      const bool ahead = at < hi && HG * tiles.upto(at, s, n, r) <= x;
-      lo += __popc(__ballot_sync(0xffffffffu, ahead)) * step;
-      hi = min(hi, lo + step);
-    }
-    t = lo;
-    x -= HG * tiles.upto(t, s, n, r);
-    const int each = count();
-    hg = (int)(x / each);
-    return (int)(x - (int64_t)hg * each);
   }
   __device__ __forceinline__ int first_row() const { return t << r; }
-  __device__ __forceinline__ int last_row() const { return (int)min((int64_t)n, ((int64_t)t + 1) << r) - 1; }
-  __device__ __forceinline__ int count() const { return tiles.count(s + first_row(), s + last_row()); }
-  // The next unit (there is one).
-  __device__ void next() {
-    if (++hg < HG) return;
+  __device__ __forceinline__ int end_row() const { return n - first_row() > (1 << r) ? first_row() + (1 << r) : n; }
+  __device__ __forceinline__ int count() const { return tiles.count(s + first_row(), s + end_row() - 1); }
+  // The current unit's part in this range: tiles [off, off + the result) of its `all` own ones; 0: none (the range
+  // ends among what it counts for beside). x is then the part's first tile.
+  __device__ __forceinline__ int part(int& all) {
+    all = count();
+    const int ahead = max(0, extra - off);
+    off = max(0, off - extra);
+    x += ahead;
+    return max(0, min(all - off, end - x));
+  }
+  // On to the next unit, behind a part of m tiles; false: the range is at its end.
+  __device__ __forceinline__ bool next(int m) {
+    x += m;
+    off = 0;
+    if (x >= end) return false;
+    if (++hg < HG) return true;
     hg = 0;
-    if (++t < units) return;
-    unsigned left = __ballot_sync(0xffffffffu, in_class(my_n) && group + lane() > b);
+    if (++t < units) return true;
+    unsigned left = __ballot_sync(0xffffffffu, mine() && group + lane() > b);
     while (!left && group + 32 < B) {
-      group += 32;
-      load(group, my_n, my_s, my_c0);
-      left = __ballot_sync(0xffffffffu, in_class(my_n));
+      load(group + 32);
+      left = __ballot_sync(0xffffffffu, mine());
     }
-    if (left) take(__ffs(left) - 1);
+    if (!left) return false;   // (there is one)
+    take(__ffs(left) - 1);
+    return true;
   }
 };
 
 size_t chunk_workspace(const medusa_cfg& c, int T);
+bool chunk_countable(const medusa_cfg& c, int T);   // key tiles of any lengths stay within 32 bits
 ChunkSpace chunk_space(const medusa_cfg& c, int T);
 cudaError_t launch_chunk_tc(const medusa_cfg& c, const void* Q, const void* Kp, const void* Vp, void* O, const ChunkArgs& a,
                             const ChunkSpace& sp, void* ws, cudaStream_t st);

@@ -65,6 +65,8 @@ constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSms = 152;
 constexpr int kLeastKeys = 256;   // of a key range that is one of several: two tiles
+// What a unit of new tokens over a paged cache counts for beside its key tiles.
+constexpr int kPairExtra = 2, kSingleExtra = 2;
 constexpr int kAhead = 8;   // steps (K and V tiles) of a unit still to be loaded when the next unit is fetched
 // The running maximum moves (and O is rescaled) only when a tile's maximum exceeds it by more
 // than this many binary orders of magnitude: weights stay below 2^8, far inside bf16 and f32.
@@ -109,10 +111,10 @@ struct Unit {
   int k0[2], kend[2];     // key range
   int n[2], tree[2];      // key tiles (the tree tile included); number of the tree tile, or -1
   int part[2];            // prefix: which partial result the tile writes; chunks: its first row there, or -1 (none: O)
-  // chunks: each half is written by a warp of its own
-  int more[2];            // 0: that warp has come to its end
+  // chunks:
   int p0[2];              // logical row of the tile's first row
   int j0[2], skip[2];     // the part's first tile among the unit's, and what they skip behind the first rows
+  int pages[2][32];       // of the part's first 32 tiles
 };
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -225,6 +227,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // One tile's part of a unit, as decoded by lanes t, t + 2, ... of the scheduling warp. (What runs
 // once per unit is kept short: between two units its instructions come from beyond the
 // instruction caches, which the softmax fills.)
@@ -295,75 +301,6 @@ __device__ __forceinline__ Piece decode_prefix(const RowsArgs& a, int u, int t) 
   return w;
 }
 
-// The units of new tokens over a paged cache that fall into this CTA's ranges: tile t of each, by a
-// warp for each t. Pairs come first, with both tiles over the same keys (both warps go through the same
-// ones); then single tiles, a stream of them for each t.
-struct ChunkFeed {
-  ChunkWalk<7> walk;
-  int64_t x, end, range;
-  int off, phase, stream;   // phase 0: pairs, 1: singles, 2: done
-
-  __device__ __forceinline__ void open(const RowsArgs& a, int t) {
-    const ChunkSpace& sp = a.space;
-    for (; phase < 2; ++phase) {
-      const int streams = phase == 0 ? sp.pair_streams : sp.streams;
-      if (streams == 0) continue;
-      const int log_npos = 31 - __clz(sp.npos);
-      if (phase == 0) walk.choose(log_npos + 1, sp.npos + 1, INT32_MAX);
-      else walk.choose(log_npos, 1, sp.npos);
-      stream = phase == 0 ? (int)blockIdx.x : t * kSms + (int)blockIdx.x;
-      const int64_t all = walk.total();
-      range = max((int64_t)1, (all + streams - 1) / streams);
-      x = min(all, stream * range);
-      end = min(all, x + range);
-      if ((threadIdx.x & 31) == 0 && (phase == 1 || t == 0))
-        a.cuts[phase == 0 ? stream : sp.pair_streams + stream] = ChunkCut{0, 0, 0, 0};
-      if (x < end) {
-        off = walk.seek(x);
-        return;
-      }
-    }
-  }
-  // This warp's half of the next unit; false: there is none.
-  __device__ __forceinline__ bool next(const RowsArgs& a, int t, Unit& d) {
-    if (phase == 2) return false;
-    const ChunkSpace& sp = a.space;
-    const int lane = threadIdx.x & 31, npos = sp.npos;
-    const int all = walk.count(), n = (int)min((int64_t)(all - off), end - x);
-    const int row0 = walk.first_row() + (phase == 0 ? t * npos : 0), left = walk.n - row0;
-    const int p_first = walk.s + walk.first_row(), skip = walk.tiles.skip(p_first);
-    const int upto = left > 0 ? ((walk.s + min(walk.n, row0 + npos) - 1) >> 7) + 1 - skip : 0;   // the tile's own tiles
-    const bool cut = off > 0 || n < all;   // (a unit that is cut writes partial results)
-    if (lane == 0) {
-      d.more[t] = 1;
-      d.dual = phase;
-      d.pos0[t] = walk.c0 + row0;
-      d.left[t] = left;
-      d.h0[t] = walk.hg << a.gp_shift;
-      d.kvh[t] = (walk.hg << a.gp_shift) / (a.Hq / a.Hkv);
-      d.base[t] = walk.b;
-      d.kend[t] = left > 0 ? walk.s + min(walk.n, row0 + npos) : 0;
-      d.n[t] = max(0, min(n, upto - off));
-      d.part[t] = !cut ? -1 : (int)(phase == 0 ? sp.pair_part(stream, off == 0) + t * kRows : sp.single_part(stream, off == 0));
-      d.p0[t] = walk.s + row0;
-      d.j0[t] = off;
-      d.skip[t] = skip;
-      if (cut && off == 0 && (phase == 1 || t == 0))
-        a.cuts[phase == 0 ? stream : sp.pair_streams + stream] =
-            ChunkCut{walk.c0 + walk.first_row(), walk.n - walk.first_row(), walk.hg << a.gp_shift, (int)((x + all - 1) / range) - stream};
-    }
-    x += n;
-    off = 0;
-    if (x < end) {
-      walk.next();
-    } else {
-      ++phase;
-      open(a, t);
-    }
-    return true;
-  }
-};
-
 template <int kD, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -373,13 +310,16 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   constexpr int kStages = Lay::stages, kTile = Lay::tile, kHalves = Lay::halves;
   constexpr bool kPrefix = kMode == kPrefixMode, kChunk = kMode == kChunkMode;
   // (Behind a prefix the next kernel's blocks, started early, would crowd the SMs that are done first.)
-  if (kMode == kPromptMode) pdl_trigger();
+  // (One CTA per SM, as many as there are, leaves nothing to crowd.)
+  if (kMode != kPrefixMode) pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = sm + Lay::ring;
   __shared__ __align__(8) uint64_t kv_full[kStages], kv_empty[kStages];
   __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_done[2];
   __shared__ __align__(8) uint64_t unit_full[2], unit_empty[2], tail, stolen, want;
+  __shared__ __align__(8) uint64_t half_full, half_free;   // chunks: the second half of a single tile's keys
+  __shared__ float2 half_ml[kChunk ? kRows : 1];           // ... its maxima and sums; its O stays in TMEM
   __shared__ __align__(16) uint4 steal_slot[1];
   __shared__ Unit units[2];
   __shared__ uint32_t tmem_slot;
@@ -404,9 +344,16 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     tc::mbar_init(&tail, 1);
     tc::mbar_init(&stolen, 1);
     tc::mbar_init(&want, 1);
+    tc::mbar_init(&half_full, kRows);
+    tc::mbar_init(&half_free, kRows);
     tc::mbar_fence_init();
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&tmem_slot, kTmemCols);
+  if (kChunk && warp == kLoadWarp && lane == 0) {
+    prefetch_map(&tmQ);
+    prefetch_map(&tmK);
+    prefetch_map(&tmV);
+  }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -421,14 +368,18 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     w = units[i & 1];
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&unit_empty[i & 1]);
-    return kChunk ? (w.more[0] | w.more[1]) != 0 : w.kind != kEnd;
+    return w.kind != kEnd;
   };
 
   if (kChunk && warp >= kPlanWarp) {
     // ------------------------------------------------------------------ schedule: ranges of the work
+    // One range of the pairs' key tiles and one of the single tiles'; tile t's half of each unit by a warp for
+    // each t (both go through the same units). Both tiles of a pair take the same keys; a single tile's keys
+    // are divided between the two, so that there is one tile's softmax to hide behind the other's products, and
+    // joined at its end. (A range of its own for each tile leaves one idle where their units differ in length.)
     const int t = warp - kPlanWarp;
-    ChunkFeed feed;
-    feed.phase = 0;
+    const ChunkSpace& sp = a.space;
+    ChunkWalk<7> walk;
     {
       ChunkArgs c{};
       c.cu = a.cu;
@@ -439,25 +390,65 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       c.Hq = a.Hq;
       c.window = a.window;
       c.sinks = a.sinks;
-      feed.walk.begin(c, a.gp_shift);
+      walk.begin(c, a.gp_shift);
     }
-    feed.open(a, t);
-    for (int i = 0;; ++i) {
-      if (i >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&unit_empty[i & 1], ((i >> 1) - 1) & 1, err, 2))) break;
-      Unit& d = units[i & 1];
-      if (!feed.next(a, t, d) && lane == 0) {   // (the other tile may still have some)
-        d.more[t] = d.n[t] = d.left[t] = 0;
-        d.dual = 1;
+    int i = 0;
+    bool ok = true;
+    auto free_slot = [&] {
+      if (i >= 2) ok = __all_sync(0xffffffffu, tc::mbar_wait(&unit_empty[i & 1], ((i >> 1) - 1) & 1, err, 2));
+      return ok;
+    };
+    for (int single = sp.pair_streams ? 0 : 1; ok && single < 2; ++single) {
+      const int log_npos = 7 - a.gp_shift;
+      ChunkCut* cut_at = a.cuts + (single ? sp.pair_streams : 0) + blockIdx.x;
+      if (lane == 0 && t == 0) *cut_at = ChunkCut{0, 0, 0, 0};
+      bool more = walk.open(single ? log_npos : log_npos + 1, single ? 1 : npos + 1, single ? npos : INT32_MAX,
+                            single ? kSingleExtra : kPairExtra, (int)blockIdx.x, kSms);
+      while (more) {
+        int all;
+        const int m = walk.part(all);
+        if (m == 0) break;
+        if (!free_slot()) break;
+        Unit& d = units[i & 1];
+        const int row0 = walk.first_row() + (single ? 0 : t * npos), left = walk.n - row0;
+        const int skip = walk.tiles.skip(walk.s + walk.first_row()), half = (m + 1) >> 1;
+        const int j0 = single && t == 1 ? walk.off + half : walk.off;
+        const bool cut = m < all;   // (a unit that is cut writes partial results)
+        if (lane == 0) {
+          d.kind = kNew;
+          d.dual = single;
+          d.pos0[t] = walk.c0 + row0;
+          d.left[t] = left;
+          d.h0[t] = walk.hg << a.gp_shift;
+          d.kvh[t] = (walk.hg << a.gp_shift) / (a.Hq / a.Hkv);
+          d.base[t] = walk.b;
+          d.k0[t] = walk.s;   // the sequence's first row, and one past its last
+          d.kend[t] = walk.s + walk.n;
+          // (a pair's first tile may be through with its keys before the part begins)
+          const int own = left > 0 ? ((walk.s + row0 + min(left, npos) - 1) >> 7) + 1 - skip - walk.off : 0;
+          d.n[t] = single ? (t == 0 ? half : m - half) : max(0, min(m, own));
+          d.part[t] = !cut ? -1 : (int)(single ? sp.single_part(blockIdx.x, walk.off == 0) : sp.pair_part(blockIdx.x, walk.off == 0) + t * kRows);
+          d.p0[t] = walk.s + row0;
+          d.j0[t] = j0;
+          d.skip[t] = skip;
+          if (cut && walk.off == 0 && t == 0)
+            *cut_at = ChunkCut{walk.c0 + row0, left, walk.hg << a.gp_shift, (walk.x + all - 1) / walk.range - (int)blockIdx.x};
+        }
+        if (j0 + lane < walk.off + m)
+          d.pages[t][lane] = a.table[(size_t)walk.b * a.max_pages + walk.tiles.tile(j0 + lane, skip) * kKeys / a.page_rows];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&unit_full[i & 1]);
+        ++i;
+        more = walk.next(m);
       }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&unit_full[i & 1]);
-      __syncwarp();
-      // both halves are there: the end is where neither has a unit
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(&unit_full[i & 1], (i >> 1) & 1, err, 1))) break;
-      const bool more = d.more[0] | d.more[1];
-      __syncwarp();
-      if (!more) break;
     }
+    if (ok && free_slot()) {
+      if (lane == 0) {
+        units[i & 1].kind = kEnd;
+        tc::mbar_arrive(&unit_full[i & 1]);
+      }
+    }
+    __syncwarp();
   } else if (warp == kPlanWarp) {
     // ------------------------------------------------------------------ schedule
     // Block indices are units in order. The CTA begins with its own and then takes over blocks
@@ -513,6 +504,134 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       tc::mbar_arrive(&unit_full[i & 1]);
     }
     __syncwarp();
+  } else if (kChunk && warp == kLoadWarp) {
+    // ------------------------------------------------------------------ TMA loads: tiles from pages
+    // In the MMA warp's order, as below. What has to wait for others is put off rather than waited for,
+    // so that copies stay in flight: a tile of rows whose place is still in use, and the zeroing of what
+    // no row of the sequence sees in a V tile that has not arrived. Both are looked after in every wait.
+    ChunkTiles<7> list;
+    list.begin(a.window, a.sinks);
+    Unit w;
+    int it = 0, nq[2] = {0, 0}, fixes = 0;   // ring position, Q tiles loaded, V tiles zeroed
+    int page_reg[2] = {-1, -1};
+    bool ok = true, q_wait[2] = {false, false}, fix_wait = false;
+    int q_pos[2] = {0, 0}, q_head[2] = {0, 0};
+    int fix_stage = 0, fix_low = 0, fix_high = 0, fix_first = 0;   // rows [low, high) and those below first stay
+    auto there = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
+    auto serve = [&] {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (q_wait[t] && (nq[t] == 0 || there(&q_empty[t], (nq[t] - 1) & 1))) {
+          if (lane == 0) {
+            uint8_t* dst = sm + t * kTile;
+            tc::mbar_arrive_expect(&q_full[t], kTile);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * kHalf, &tmQ, 64 * h, q_pos[t], q_head[t], &q_full[t]);
+          }
+          ++nq[t];
+          q_wait[t] = false;
+        }
+      if (fix_wait && there(&tail, fixes & 1)) {
+        uint8_t* dst = ring + fix_stage * kTile;
+#pragma unroll 1
+        for (int c = lane; c < kKeys * 8; c += 32) {
+          const int row = c >> 3;
+          if (row < fix_high && (row >= fix_low || row < fix_first)) continue;
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) reinterpret_cast<uint4*>(dst + h * kHalf)[c] = make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&kv_full[fix_stage]);
+        ++fixes;
+        fix_wait = false;
+      }
+    };
+    // until `done` says so, serving meanwhile; false when the wait ran out. (It polls: with waits that may be
+    // suspended 2048 rows after 14336 took 370 us instead of 354.)
+    auto until = [&](auto done, uint32_t code) {
+      const long long t0 = clock64();
+      for (;;) {
+        serve();
+        if (done()) return true;
+        if (__any_sync(0xffffffffu, clock64() - t0 > 4000000000LL)) {
+          if (lane == 0) atomicOr(err, code);
+          return false;
+        }
+      }
+    };
+    for (int i = 0; ok; ++i) {
+      ok = until([&] { return there(&unit_full[i & 1], (i >> 1) & 1); }, 1);
+      if (!ok) break;
+      w = units[i & 1];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) page_reg[t] = units[i & 1].pages[t][lane];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&unit_empty[i & 1]);
+      if (w.kind == kEnd) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (w.n[t] > 0) {
+          if (q_wait[t]) ok = ok && until([&] { return !q_wait[t]; }, 4);
+          q_wait[t] = true;
+          q_pos[t] = w.pos0[t];
+          q_head[t] = w.h0[t];
+        }
+      const int nt = max(w.n[0], w.n[1]), tiles = w.dual ? 2 : 1;
+#pragma unroll 1
+      for (int j = nt > 0 ? -1 : 0; ok && j < nt; ++j) {   // step j: V_j and K_{j+1}
+#pragma unroll 1
+        for (int x = 0; ok && x < 2 * tiles; ++x) {
+          const int t = x >> 1, n = w.dual ? (t ? w.n[1] : w.n[0]) : nt, jt = j + (x & 1);
+          const bool isv = !(x & 1);
+          if (jt < 0 || jt >= n) continue;
+          const int base = t ? w.base[1] : w.base[0], kvh = t ? w.kvh[1] : w.kvh[0];
+          const int skip = t ? w.skip[1] : w.skip[0], j0 = t ? w.j0[1] : w.j0[0];
+          const int st = it % kStages;
+          ok = until([&] { return it < kStages || there(&kv_empty[st], (it / kStages - 1) & 1); }, 8);
+          if (!ok) break;
+          const int key0 = list.tile(j0 + jt, skip) * kKeys;
+          int pages = t ? page_reg[1] : page_reg[0];
+          if (!isv && (jt & 31) == 0 && jt > 0) {   // 32 tiles' pages at a time, one per lane (the first come with the unit)
+            pages = jt + lane < n ? a.table[(size_t)base * a.max_pages + list.tile(j0 + jt + lane, skip) * kKeys / a.page_rows] : -1;
+            if (t) page_reg[1] = pages;
+            else page_reg[0] = pages;
+          }
+          const int page = __shfl_sync(0xffffffffu, pages, jt & 31);
+          const bool in_pool = page >= 0 && page < a.num_pages;
+          MEDUSA_CHECK(isv || lane != 0 || in_pool, MEDUSA_CHECK_PAGE);
+          // (what other rows of the sequence see stays: it is theirs that it holds numbers)
+          const int low = max(0, w.k0[0] - a.window + 1) - key0, first = a.sinks - key0, high = w.kend[0] - key0;
+          const bool fix = isv && (high < kKeys || (low > 0 && first < min(low, kKeys)));
+          if (fix) {
+            if (fix_wait) ok = until([&] { return !fix_wait; }, 16);
+            if (!ok) break;
+            fix_wait = true;
+            fix_stage = st;
+            fix_low = low;
+            fix_high = high;
+            fix_first = first;
+          }
+          if (lane == 0) {
+            uint8_t* dst = ring + st * kTile;
+            uint64_t* bar = fix ? &tail : &kv_full[st];
+            const int y = key0 % a.page_rows, z = (in_pool ? page : a.num_pages) * a.Hkv + kvh;   // outside the pool: zeros
+            tc::mbar_arrive_expect(bar, kTile);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * kHalf, isv ? &tmV : &tmK, 64 * h, y, z, bar);
+          }
+          __syncwarp();
+          ++it;
+        }
+      }
+    }
+    if (ok) until([&] { return !q_wait[0] && !q_wait[1] && !fix_wait; }, 16);
+    // never leave with copies still landing in shared memory
+    if (fix_wait) tc::mbar_wait(&tail, fixes & 1, err, 16);
+    for (int x = it > kStages ? it - kStages : 0; x < it; ++x)
+      if (!(fix_wait && x % kStages == fix_stage)) tc::mbar_wait(&kv_full[x % kStages], (x / kStages) & 1, err, 32);
+    for (int t = 0; t < 2; ++t)
+      if (nq[t] > 0) tc::mbar_wait(&q_full[t], (nq[t] - 1) & 1, err, 64);
   } else if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ TMA loads
     // Tiles come in the order in which the MMA warp uses them: K_0, V_0, K_1, V_1, ...; for two
@@ -520,25 +639,21 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     Unit w;
     int it = 0, nq[2] = {0, 0}, fixes = 0;   // ring position, Q tiles loaded, tails zeroed
     int page_reg[2] = {-1, -1};
-    ChunkTiles<7> list;
-    list.window = a.window;
-    list.sink_tiles = (int)(((unsigned)a.sinks + (kKeys - 1)) / kKeys);
     int seen = -1;   // prefix: shared rows that any sequence sees (once it is known: rows past it may hold anything)
     bool ok = true;
     for (int i = 0; ok && next_unit(i, w); ++i) {
       const int nt = max(w.n[0], w.n[1]), tiles = w.dual ? 2 : 1;
-      if (!kChunk && nt <= kAhead && lane == 0) tc::mbar_arrive(&want);   // time to fetch the next unit
+      if (nt <= kAhead && lane == 0) tc::mbar_arrive(&want);   // time to fetch the next unit
 #pragma unroll 1
       for (int j = nt > 0 ? -1 : 0; ok && j < nt; ++j) {   // step j: V_j and K_{j+1}
-        if (!kChunk && j > 0 && nt - j == kAhead && lane == 0) tc::mbar_arrive(&want);
+        if (j > 0 && nt - j == kAhead && lane == 0) tc::mbar_arrive(&want);
 #pragma unroll 1
         for (int x = 0; ok && x < 2 * tiles; ++x) {
           const int t = x >> 1, n = w.dual ? (t ? w.n[1] : w.n[0]) : nt, jt = j + (x & 1);
           const bool isv = !(x & 1);
           if (jt < 0 || jt >= n) continue;
           // a tile's rows go ahead of its first K tile; tile 1's, where both share the keys, behind it
-          // (a part of a pair may have none of tile 0's keys)
-          const int r = j < 0 ? (kChunk && w.n[0] == 0 ? (w.dual ? t : -1) : t) : (j == 0 && x == 0 && !w.dual && w.n[1] > 0) ? 1 : -1;
+          const int r = j < 0 ? t : (j == 0 && x == 0 && !w.dual && w.n[1] > 0) ? 1 : -1;
           if (r >= 0) {
             const int used = r ? nq[1] : nq[0];
             if (used > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty[r], (used - 1) & 1, err, 4));
@@ -559,10 +674,9 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           if (it >= kStages) ok = __all_sync(0xffffffffu, tc::mbar_wait<true>(&kv_empty[st], (it / kStages - 1) & 1, err, 8));
           if (!ok) break;
           const bool tree = kPrefix && jt == (t ? w.tree[1] : w.tree[0]);
-          const int skip = t ? w.skip[1] : w.skip[0], j0 = t ? w.j0[1] : w.j0[0];
-          const int key0 = kChunk ? list.tile(j0 + jt, skip) * kKeys : k0 + jt * kKeys;
+          const int key0 = k0 + jt * kKeys;
           int y, z;
-          if (kMode == kPromptMode) {
+          if (!kPrefix) {
             y = base + key0;
             z = kvh;
           } else if (tree) {
@@ -571,10 +685,10 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           } else {
             int pages = t ? page_reg[1] : page_reg[0];
             if (!isv && (jt & 31) == 0) {   // 32 tiles' pages at a time, one per lane
-              const int key = kChunk ? list.tile(j0 + jt + lane, skip) * kKeys : key0 + lane * kKeys;
+              const int key = key0 + lane * kKeys;
               pages = -1;
-              if (kChunk ? jt + lane < n : key < kend)
-                pages = !kChunk && w.kind == kShared ? a.prefix[key / a.page_rows] : a.table[(size_t)base * a.max_pages + key / a.page_rows];
+              if (key < kend)
+                pages = w.kind == kShared ? a.prefix[key / a.page_rows] : a.table[(size_t)base * a.max_pages + key / a.page_rows];
               if (t) page_reg[1] = pages;
               else page_reg[0] = pages;
             }
@@ -596,11 +710,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           }
           const int last = kPrefix && w.kind == kShared ? min(kend, seen) : kend;
           const int live = tree ? kKeys : max(0, min(kKeys, last - key0));   // (rows past the tree's nodes arrive as zeros)
-          // chunks: what no row of the unit sees (a part's tiles are of a pair: tile 0's first row, tile 1's last)
-          const int low = kChunk ? max(0, (t ? w.p0[1] : w.p0[0]) - a.window + 1) - key0 : 0;
-          const int high = kChunk ? min(kKeys, (w.dual ? kend : max(w.kend[0], w.kend[1])) - key0) : live;
-          const int first = kChunk ? a.sinks - key0 : 0;   // rows below it stay visible
-          const bool fix = isv && (high < kKeys || (kChunk && low > 0 && first < min(low, kKeys)));
+          const bool fix = isv && live < kKeys;
           uint64_t* bar = fix ? &tail : &kv_full[st];
           if (lane == 0) {
             tc::mbar_arrive_expect(bar, kTile);
@@ -613,8 +723,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             ++fixes;
             if (!ok) break;
 #pragma unroll 1
-            for (int c = (kChunk ? 0 : live * 8) + lane; c < kKeys * 8; c += 32) {
-              if (kChunk && (c >> 3) < high && ((c >> 3) >= low || (c >> 3) < first)) continue;
+            for (int c = live * 8 + lane; c < kKeys * 8; c += 32) {
 #pragma unroll
               for (int h = 0; h < kHalves; ++h) reinterpret_cast<uint4*>(dst + h * kHalf)[c] = make_uint4(0, 0, 0, 0);
             }
@@ -739,9 +848,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             // 1's last, if everything for it is there.
             if (ok && t == 0 && !dual && j + 1 == nt && mbar_test(&unit_full[(i + 1) & 1], ((i + 1) >> 1) & 1)) {
               const int n0 = units[(i + 1) & 1].n[0];
-              const bool on = kChunk ? (units[(i + 1) & 1].more[0] | units[(i + 1) & 1].more[1]) != 0 && !units[(i + 1) & 1].dual
-                                     : units[(i + 1) & 1].kind != kEnd;
-              if (on && n0 > 0 && mbar_test(&kv_full[st], ph) && mbar_test(&q_full[0], nq[0] & 1)) {
+              if (units[(i + 1) & 1].kind != kEnd && (!kChunk || !units[(i + 1) & 1].dual) && n0 > 0 && mbar_test(&kv_full[st], ph) && mbar_test(&q_full[0], nq[0] & 1)) {
                 tc::fence_after();
                 ++nq[0];
                 issue_S(0, st);
@@ -759,8 +866,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       for (int i = 0; ok; ++i) {
         ok = tc::mbar_wait(&unit_full[i & 1], (i >> 1) & 1, err, 1);
         if (!ok) break;
-        const bool end = kChunk ? !(units[i & 1].more[0] | units[i & 1].more[1]) : units[i & 1].kind == kEnd;
-        const bool two = units[i & 1].dual;
+        const bool end = units[i & 1].kind == kEnd, two = units[i & 1].dual;
         const int n[2] = {units[i & 1].n[0], units[i & 1].n[1]};
         tc::mbar_arrive(&unit_empty[i & 1]);
         if (end) break;
@@ -777,21 +883,25 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const uint32_t tS = tmem + col_S(t) + lanes, tO = tmem + col_O(t) + lanes;
     const int rhead = row >> (7 - a.gp_shift), rpos = row & (npos - 1);
     ChunkTiles<7> list;
-    list.window = a.window;
-    list.sink_tiles = (int)(((unsigned)a.sinks + (kKeys - 1)) / kKeys);
+    list.begin(a.window, a.sinks);
     int ns = 0, nu = 0;   // S tiles and units taken
-    bool ok = true;
+    int halves = 0;       // chunks: single tiles taken
+    bool ok = true, lent = false;   // lent: tile 1's last O has yet to be read by tile 0's warps
+    // tile 1's O may be written again
+    auto back = [&] {
+      if (kChunk && lent) ok = __all_sync(0xffffffffu, tc::mbar_wait(&half_free, (halves - 1) & 1, err, 32768));
+      lent = false;
+    };
     for (int i = 0; ok; ++i) {
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&unit_full[i & 1], (i >> 1) & 1, err, 1));
       if (!ok) break;
       const Unit& w = units[i & 1];
       const int kind = w.kind, n = w.n[t], k0 = w.k0[t], kend = w.kend[t], tree_tile = w.tree[t], left = w.left[t];
       const int pos = w.pos0[t] + rpos, head = w.h0[t] + rhead, base = w.base[t], part_no = w.part[t];
-      const bool end = kChunk ? !(w.more[0] | w.more[1]) : kind == kEnd;
       const int p = w.p0[t] + rpos, j0 = w.j0[t], skip = w.skip[t], single = w.dual;   // chunks
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&unit_empty[i & 1]);
-      if (end) break;
+      if (kind == kEnd) break;
       const bool row_ok = rpos < left;
       // keys below `limit` are visible to this row
       int limit = kend;
@@ -837,7 +947,10 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
               const int here = vis - 32 * c;
               auto below = [](int x) { return x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1u; };
               if (!tree) see[c] = below(here);
-              if (kChunk) see[c] &= ~below(low - key0 - 32 * c) | below(a.sinks - key0 - 32 * c);
+              if (kChunk) {
+                see[c] &= ~below(low - key0 - 32 * c) | below(a.sinks - key0 - 32 * c);
+                if (!__any_sync(0xffffffffu, row_ok && see[c] != 0xffffffffu)) continue;
+              }
 #pragma unroll
               for (int x = 0; x < 32; ++x)
                 v[32 * c + x] = (see[c] >> x) & 1u ? v[32 * c + x] : __float_as_uint(-INFINITY);
@@ -875,6 +988,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           }
           tc::tmem_wait_st();
           tc::fence_before();
+          back();
           tc::mbar_arrive(&p_half[t]);   // the product with V begins on these 64 keys
           const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
 #pragma unroll
@@ -887,6 +1001,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           tc::tmem_wait_st();
           tc::fence_before();
         } else {
+          back();
           tc::mbar_arrive(&p_half[t]);
         }
         tc::mbar_arrive(&p_full[t]);
@@ -898,7 +1013,50 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         if (!ok) break;
         tc::fence_after();
       }
-      if (!busy) continue;
+      float w0 = 1.f, w1 = 0.f;   // chunks: what O_0 and O_1 are multiplied with
+      if (kChunk && single) {
+        if (t == 1) {   // tile 0's warps take it from here
+          back();       // (where this unit gave tile 1 no keys)
+          if (!ok) break;
+          half_ml[row] = make_float2(m_run, l_run);
+          tc::fence_before();
+          tc::mbar_arrive(&half_full);
+          ++halves;
+          lent = true;
+          continue;
+        }
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&half_full, halves & 1, err, 65536));
+        ++halves;
+        if (!ok) break;
+        tc::fence_after();
+        const float2 other = half_ml[row];
+        if (!(other.x == -INFINITY && other.y == 0.f)) {   // (else nothing was visible there)
+          const float M = fmaxf(m_run, other.x), mu = M == -INFINITY ? 0.f : M;
+          w0 = tc::ex2(m_run - mu);
+          w1 = tc::ex2(other.x - mu);
+          l_run = l_run * w0 + other.y * w1;
+          m_run = M;
+        }
+      }
+      const bool both = kChunk && __any_sync(0xffffffffu, w1 != 0.f);   // (or no number)
+      // a part of O: 32 columns from c on
+      auto load_O = [&](int c, uint32_t* o) {
+        tc::tmem_ld32(tO + 32 * c, o);
+        tmem_landed32(o);
+        if (!both) return;
+        uint32_t o1[32];
+        tc::tmem_ld32(tO + col_O(1) - col_O(0) + 32 * c, o1);
+        tmem_landed32(o1);
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          const float first = __uint_as_float(o[x]) * w0;
+          o[x] = __float_as_uint(w1 == 0.f ? first : fmaf(__uint_as_float(o1[x]), w1, first));
+        }
+      };
+      if (!busy) {
+        if (kChunk && single) tc::mbar_arrive(&half_free);
+        continue;
+      }
       // Four lanes hold four consecutive positions of one head. They trade 16-byte pieces, so that
       // a store instruction writes 64 bytes of each row, not 16 (a quarter of the memory lines).
       const int quad = lane & 3;
@@ -910,8 +1068,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 #pragma unroll 1
         for (int c = 0; c < kD / 32; ++c) {
           uint32_t o[32], pk[16];
-          tc::tmem_ld32(tO + 32 * c, o);
-          tmem_landed32(o);
+          load_O(c, o);
 #pragma unroll
           for (int x = 0; x < 16; ++x)
             pk[x] = pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
@@ -932,8 +1089,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 #pragma unroll 1
           for (int c = 0; c < kD / 32; ++c) {
             uint32_t o[32];
-            tc::tmem_ld32(tO + 32 * c, o);
-            tmem_landed32(o);
+            load_O(c, o);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               transpose4(o + 16 * x);
@@ -952,6 +1108,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
       }
       tc::fence_before();   // O has been read before the next unit's first P is announced
+      if (kChunk && single) tc::mbar_arrive(&half_free);
     }
   }
 
