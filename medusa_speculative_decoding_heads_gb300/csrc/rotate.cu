@@ -6,13 +6,15 @@
 //
 // D / 8 lanes hold a head, 8 head dims each, in two pieces of 4 that lie so that both dims of a pair
 // are in the same lane: R / 2 apart where halves turn against each other, next to each other where
-// neighbours do. A group of such lanes takes up to kHeads<T> heads of one token: all of them are on
-// their way while the lane works out its 4 angles, which the heads share.
+// neighbours do. A group of such lanes takes up to H heads of one token: all of them are on their way
+// while the lane works out its 4 angles, which the heads share. As many blocks as the SMs hold go
+// through the groups, so that what depends on a lane's frequencies alone is worked out once.
 //
 // Angles. pos f in float32 is off by 2^-25 pos f, 0.03 at a position of a million; here f / 2 pi
-// becomes a 64-bit fraction of a turn (from a product in 64 bits: off by 2^-52 f), so that pos times it
-// modulo 2^64 is the exact remainder. Its nearest quarter turn is taken off, and the rest, |a| <=
-// pi / 4, goes into the Taylor series of sine and cosine (to a^9 and a^10: off by 2e-9 and 2e-10).
+// becomes a 64-bit fraction of a turn, in whole numbers (off by 2^-64 of itself, and of a turn), so that
+// pos times it modulo 2^64 is the remainder. Its nearest quarter turn is taken off, and the rest, |a| <=
+// pi / 4, goes into the Taylor series of sine and cosine (to a^9 and a^10: off by 2e-9 and 2e-10). (The
+// fraction from a product in float64, for each group: 8191 tokens of 40/40 heads 121 us.)
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -22,8 +24,7 @@
 namespace medusa {
 namespace {
 
-constexpr int kThreads = 128;
-template <typename T> constexpr int kHeads = sizeof(T) == 2 ? 8 : 4;   // heads of a group: 32 registers on their way
+constexpr int kThreads = 128, kBlocks = 152 * 8;
 
 struct RotateArgs {
   const void *Q, *K, *qw, *kw;
@@ -37,12 +38,11 @@ struct RotateArgs {
   float eps;
 };
 
-// 4 values, unpacked.
+// 4 values as they come, and unpacked.
 __device__ __forceinline__ float4 get4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 get4(const uint16_t* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-}
+__device__ __forceinline__ uint2 get4(const uint16_t* p) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ float4 values(const float4& w) { return w; }
+__device__ __forceinline__ float4 values(const uint2& w) { return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)); }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -53,12 +53,20 @@ __device__ __forceinline__ void put4(uint16_t* p, const float4& v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
 }
 
-// (cos, sin) of pos * freq.
-__device__ __forceinline__ float2 turn_of(float freq, int pos) {
-  double t = (double)freq * 0.15915494309189533577;   // turns per position: f / 2 pi
-  t -= rint(t);
-  if (!(fabs(t) <= 0.5)) return make_float2(NAN, NAN);   // (a frequency that is no finite number)
-  const uint64_t turns = (uint64_t)__double2ll_rn(t * 9223372036854775808.0) * 2u * (uint64_t)(int64_t)pos;   // 2^64 to a turn
+// freq / 2 pi in 2^-64 turns, modulo a turn: freq is m 2^e, and m times 2^66 / 2 pi has 88 bits.
+__device__ __forceinline__ uint64_t turns_of(float freq) {
+  const uint32_t bits = __float_as_uint(freq), field = (bits >> 23) & 255u;
+  const uint64_t m = (bits & 0x7fffffu) | (field ? 0x800000u : 0u), c = 0xa2f9836e4e44152aull;   // 2^66 / 2 pi
+  const uint64_t lo = m * c, hi = __umul64hi(m, c);
+  const int s = 152 - (int)(field ? field : 1u);   // to the right by 2 - e
+  uint64_t f;
+  if (s <= 0) f = s > -64 ? lo << -s : 0;
+  else if (s < 64) f = lo >> s | hi << (64 - s);
+  else f = s < 128 ? hi >> (s - 64) : 0;
+  return bits >> 31 ? 0 - f : f;
+}
+// (cos, sin) of the angle of `turns` 2^-64 turns.
+__device__ __forceinline__ float2 turn(uint64_t turns) {
   const int h = (int)(turns >> 32), quarter = (int)((uint32_t)h + (1u << 29)) >> 30;
   const int rest = (int)((uint32_t)h - ((uint32_t)quarter << 30));
   const float a = (float)rest * 1.4629180792671596e-9f;   // pi 2^-31
@@ -76,97 +84,124 @@ __device__ __forceinline__ float2 turn_of(float freq, int pos) {
   return make_float2(((quarter + 1) & 2) ? -x : x, (quarter & 2) ? -y : y);
 }
 
-template <typename T, int D>
+template <typename T, int D, int H>
 __global__ void __launch_bounds__(kThreads)
 qk_norm_rotate_kernel(const RotateArgs a) {
-  constexpr int kLanes = D / 8, H = kHeads<T>;
+  constexpr int kLanes = D / 8;
   const int l = threadIdx.x % kLanes;
-  const int64_t g = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes;
   pdl_wait();
   pdl_trigger();
-  if (g >= a.groups) return;   // (whole groups: the shuffles below name a group's lanes only)
   const unsigned mask = (kLanes == 32 ? 0xffffffffu : ((1u << kLanes) - 1u)) << ((threadIdx.x & 31) / kLanes * kLanes);
-  const int64_t t = g / a.per_token;
-  const int of = (int)(g - t * a.per_token);
-  const bool isq = of < a.q_groups;
-  const int h0 = (isq ? of : of - a.q_groups) * H, heads = min(H, (isq ? a.Hq : a.Hkv) - h0);
-  // the lane's two pieces
+  // the lane's two pieces and its frequencies
   const bool turns = 8 * l < a.R;
   const int c0 = a.pairs ? 8 * l : turns ? 4 * l : 8 * l, c1 = a.pairs || !turns ? c0 + 4 : (a.R >> 1) + 4 * l;
-  const T* src = static_cast<const T*>(isq ? a.Q : a.K) + t * (isq ? a.qs : a.ks) + (int64_t)h0 * D;
-  float4 x0[H], x1[H];
-#pragma unroll
-  for (int i = 0; i < H; ++i)
-    if (i < heads) {
-      x0[i] = get4(src + i * D + c0);
-      x1[i] = get4(src + i * D + c1);
-    }
-  const T* w = static_cast<const T*>(isq ? a.qw : a.kw);
-  float4 w0, w1;
-  if (w) {
-    w0 = get4(w + c0);
-    w1 = get4(w + c1);
-  }
-  float2 cs[4];
+  uint64_t f[4];
+  bool number[4] = {true, true, true, true};
   if (turns) {
-    const int pos = a.pos[t];
-    const float4 f = *reinterpret_cast<const float4*>(a.freq + 4 * l);
-    cs[0] = turn_of(f.x, pos);
-    cs[1] = turn_of(f.y, pos);
-    cs[2] = turn_of(f.z, pos);
-    cs[3] = turn_of(f.w, pos);
-  }
-  T* dst;
-  int64_t step = D;
-  if (isq) {
-    dst = static_cast<T*>(a.Qo) + t * a.qos + (int64_t)h0 * D;
-  } else if (a.kos) {
-    dst = static_cast<T*>(a.Ko) + t * a.kos + (int64_t)h0 * D;
-  } else {
-    const int64_t b = t / a.N;
-    dst = static_cast<T*>(a.Ko) + ((b * a.Hkv + h0) * a.N + (t - b * a.N)) * D;
-    step = (int64_t)a.N * D;
-  }
+    const float4 w = *reinterpret_cast<const float4*>(a.freq + 4 * l);
+    const float x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < H; ++i) {
-    if (i >= heads) break;
-    float4 &u = x0[i], &v = x1[i];
-    if (w) {
-      float s = u.x * u.x;
-      s = fmaf(u.y, u.y, s);
-      s = fmaf(u.z, u.z, s);
-      s = fmaf(u.w, u.w, s);
-      s = fmaf(v.x, v.x, s);
-      s = fmaf(v.y, v.y, s);
-      s = fmaf(v.z, v.z, s);
-      s = fmaf(v.w, v.w, s);
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
-      const float r = rsqrtf(fmaf(s, 1.f / D, a.eps));
-      u = make_float4(u.x * r * w0.x, u.y * r * w0.y, u.z * r * w0.z, u.w * r * w0.w);
-      v = make_float4(v.x * r * w1.x, v.y * r * w1.y, v.z * r * w1.z, v.w * r * w1.w);
+    for (int i = 0; i < 4; ++i) {
+      f[i] = turns_of(x[i]);
+      number[i] = isfinite(x[i]);
     }
+  }
+  // (whole groups leave the loop: the shuffles name a group's lanes only)
+  for (int64_t g = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / kLanes; g < a.groups; g += (int64_t)gridDim.x * (kThreads / kLanes)) {
+    const int t = (int)((uint32_t)g / (uint32_t)a.per_token), of = (int)g - t * a.per_token;   // (groups are counted in 31 bits)
+    const bool isq = of < a.q_groups;
+    const int h0 = (isq ? of : of - a.q_groups) * H, heads = min(H, (isq ? a.Hq : a.Hkv) - h0);
+    const T* src = static_cast<const T*>(isq ? a.Q : a.K) + t * (isq ? a.qs : a.ks) + (int64_t)h0 * D;
+    decltype(get4(src)) x0[H], x1[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i)
+      if (i < heads) {
+        x0[i] = get4(src + i * D + c0);
+        x1[i] = get4(src + i * D + c1);
+      }
+    const T* w = static_cast<const T*>(isq ? a.qw : a.kw);
+    float4 w0, w1;
+    if (w) {
+      w0 = values(get4(w + c0));
+      w1 = values(get4(w + c1));
+    }
+    float2 cs[4];
     if (turns) {
-      auto turn = [](float& p, float& q, const float2& c) {
-        const float x = p * c.x - q * c.y;
-        q = q * c.x + p * c.y;
-        p = x;
-      };
-      if (a.pairs) {
-        turn(u.x, u.y, cs[0]);
-        turn(u.z, u.w, cs[1]);
-        turn(v.x, v.y, cs[2]);
-        turn(v.z, v.w, cs[3]);
-      } else {
-        turn(u.x, v.x, cs[0]);
-        turn(u.y, v.y, cs[1]);
-        turn(u.z, v.z, cs[2]);
-        turn(u.w, v.w, cs[3]);
+      const uint64_t pos = (uint64_t)(int64_t)a.pos[t];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        cs[i] = turn(f[i] * pos);
+        if (!number[i]) cs[i] = make_float2(NAN, NAN);
       }
     }
-    put4(dst + i * step + c0, u);
-    put4(dst + i * step + c1, v);
+    T* dst;
+    int64_t step = D;
+    if (isq) {
+      dst = static_cast<T*>(a.Qo) + t * a.qos + (int64_t)h0 * D;
+    } else if (a.kos) {
+      dst = static_cast<T*>(a.Ko) + t * a.kos + (int64_t)h0 * D;
+    } else {
+      const int64_t b = t / a.N;
+      dst = static_cast<T*>(a.Ko) + ((b * a.Hkv + h0) * a.N + (t - b * a.N)) * D;
+      step = (int64_t)a.N * D;
+    }
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      if (i >= heads) break;
+      float4 u = values(x0[i]), v = values(x1[i]);
+      if (w) {
+        float s = u.x * u.x;
+        s = fmaf(u.y, u.y, s);
+        s = fmaf(u.z, u.z, s);
+        s = fmaf(u.w, u.w, s);
+        s = fmaf(v.x, v.x, s);
+        s = fmaf(v.y, v.y, s);
+        s = fmaf(v.z, v.z, s);
+        s = fmaf(v.w, v.w, s);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
+        const float r = rsqrtf(fmaf(s, 1.f / D, a.eps));
+        u = make_float4(u.x * r * w0.x, u.y * r * w0.y, u.z * r * w0.z, u.w * r * w0.w);
+        v = make_float4(v.x * r * w1.x, v.y * r * w1.y, v.z * r * w1.z, v.w * r * w1.w);
+      }
+      if (turns) {
+        auto both = [](float& p, float& q, const float2& c) {
+          const float x = p * c.x - q * c.y;
+          q = q * c.x + p * c.y;
+          p = x;
+        };
+        if (a.pairs) {
+          both(u.x, u.y, cs[0]);
+          both(u.z, u.w, cs[1]);
+          both(v.x, v.y, cs[2]);
+          both(v.z, v.w, cs[3]);
+        } else {
+          both(u.x, v.x, cs[0]);
+          both(u.y, v.y, cs[1]);
+          both(u.z, v.z, cs[2]);
+          both(u.w, v.w, cs[3]);
+        }
+      }
+      put4(dst + i * step + c0, u);
+      put4(dst + i * step + c1, v);
+    }
   }
+}
+
+template <typename T, int D, int H>
+cudaError_t run(const medusa_cfg& c, RotateArgs a, int T_, cudaStream_t st) {
+  a.q_groups = (c.Hq + H - 1) / H;
+  a.per_token = a.q_groups + (c.Hkv + H - 1) / H;
+  a.groups = (int64_t)T_ * a.per_token;
+  constexpr int per_block = kThreads * 8 / D;
+  const int64_t blocks = (a.groups + per_block - 1) / per_block;
+  const cudaError_t e = launch_pdl(qk_norm_rotate_kernel<T, D, H>, (unsigned)(blocks < kBlocks ? blocks : kBlocks), kThreads, 0, st, a);
+  note_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <typename T, int H>
+cudaError_t run(const medusa_cfg& c, const RotateArgs& a, int T_, cudaStream_t st) {
+  return c.D == 64 ? run<T, 64, H>(c, a, T_, st) : run<T, 128, H>(c, a, T_, st);
 }
 
 }  // namespace
@@ -175,7 +210,6 @@ cudaError_t launch_qk_norm_rotate(const medusa_cfg& c, const void* Q, const void
                                   const void* q_weight, const void* k_weight, float eps, const float* inv_freq, int rot_dim,
                                   int pairing, const int32_t* pos, void* Qo, void* Ko, int64_t qo_stride, int64_t ko_stride,
                                   cudaStream_t st) {
-  const int H = c.dtype == MEDUSA_F32 ? kHeads<float> : kHeads<uint16_t>;
   RotateArgs a{};
   a.Q = Q;
   a.K = K;
@@ -189,21 +223,13 @@ cudaError_t launch_qk_norm_rotate(const medusa_cfg& c, const void* Q, const void
   a.kos = ko_stride;
   a.freq = inv_freq;
   a.pos = pos;
-  a.q_groups = (c.Hq + H - 1) / H;
-  a.per_token = a.q_groups + (c.Hkv + H - 1) / H;
-  a.groups = (int64_t)T * a.per_token;
   a.Hq = c.Hq;
   a.Hkv = c.Hkv;
   a.N = tree_shape(c).N;
   a.R = rot_dim;
   a.pairs = pairing == MEDUSA_ROTATE_PAIRS;
   a.eps = eps;
-  const int per_block = kThreads * 8 / c.D;
-  const auto kernel = c.dtype == MEDUSA_F32 ? (c.D == 64 ? qk_norm_rotate_kernel<float, 64> : qk_norm_rotate_kernel<float, 128>)
-                                            : (c.D == 64 ? qk_norm_rotate_kernel<uint16_t, 64> : qk_norm_rotate_kernel<uint16_t, 128>);
-  const cudaError_t e = launch_pdl(kernel, (unsigned)((a.groups + per_block - 1) / per_block), kThreads, 0, st, a);
-  note_launches(1);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return c.dtype == MEDUSA_F32 ? run<float, 4>(c, a, T, st) : run<uint16_t, 8>(c, a, T, st);
 }
 
 }  // namespace medusa
