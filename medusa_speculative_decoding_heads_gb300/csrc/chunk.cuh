@@ -16,6 +16,8 @@
 
 namespace medusa {
 
+constexpr int kChunkStreams = 152;   // one CTA per SM
+
 struct ChunkArgs {
   const int32_t* cu;      // [B + 1]
   const int32_t* start;   // [B], or NULL: 0
@@ -34,7 +36,8 @@ struct ChunkCut {
 };
 
 // Partial results. Two classes of units: `pairs`, two tiles of npos positions over the same keys, of
-// sequences with more than npos rows; `singles`, one tile, of the others. (float32: one class.)
+// sequences with more than npos rows; `singles`, one tile, of the others. (float32: one tile, of
+// sequences with more than one row, and up to 4 heads of single tokens.)
 struct ChunkSpace {
   int gp_shift, npos;          // query heads of a tile (log2), positions of a tile
   int pair_streams, pair_rows; // streams, and rows of one partial result
@@ -228,6 +231,8 @@ struct ChunkWalk {
 size_t chunk_workspace(const medusa_cfg& c, int T);
 bool chunk_countable(const medusa_cfg& c, int T);   // key tiles of any lengths stay within 32 bits
 ChunkSpace chunk_space(const medusa_cfg& c, int T);
+cudaError_t launch_chunk_f32(const medusa_cfg& c, const void* Q, const void* Kp, const void* Vp, void* O, const ChunkArgs& a,
+                             const ChunkSpace& sp, void* ws, cudaStream_t st);
 cudaError_t launch_chunk_tc(const medusa_cfg& c, const void* Q, const void* Kp, const void* Vp, void* O, const ChunkArgs& a,
                             const ChunkSpace& sp, void* ws, cudaStream_t st);
 cudaError_t launch_chunk_attention(const medusa_cfg& c, const void* Q, const void* Kp, const void* Vp, void* O, const ChunkArgs& a,

@@ -963,8 +963,12 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           const bool move = m_tile > m_run + kLazy && (!kChunk || row_ok);   // also on the first visible tile (m_run = -inf): corr = 0
           if (__any_sync(0xffffffffu, move)) {
             if (move) {
-              corr = tc::ex2(m_run - m_tile);
-              m_run = m_tile;
+              // Chunks: as far above the maximum as it may come to lie below it. The first keys that a row sees
+              // may be a few first rows or the edge of a window, whose maximum is soon exceeded (weights
+              // between 2^-8 and 2^8 are as exact as those up to 1).
+              const float m_new = kChunk ? m_tile + kLazy : m_tile;
+              corr = tc::ex2(m_run - m_new);
+              m_run = m_new;
             }
             if (j > 0) {   // O += P_{j-1} V_{j-1} was issued before S_j and has landed with it
 #pragma unroll 1
