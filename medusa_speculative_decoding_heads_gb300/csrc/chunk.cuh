@@ -65,6 +65,14 @@ struct ChunkTiles {
   __device__ __forceinline__ int tile(int j, int skipped) const { return j < sink_tiles ? j : j + skipped; }
 };
 
+// A part of a unit: `m` of its `all` tiles, from number `off` on.
+struct ChunkPart {
+  int b, s, n, c0;        // the sequence, its first logical row, rows, first packed row
+  int row, hg;            // the unit's first row of them, its group of query heads
+  int off, m, all, x;     // x: where among all tiles it begins
+  __device__ __forceinline__ bool cut() const { return m < all; }   // (a unit that is cut writes partial results)
+};
+
 // A stream's units of one class, one after another; a whole warp calls every function. (What it does ahead
 // of the first unit is time without any: its code is short, and counted in 32 bits, which the host has checked.)
 template <int kShift>
@@ -200,14 +208,22 @@ struct ChunkWalk {
   __device__ __forceinline__ int first_row() const { return t << r; }
   __device__ __forceinline__ int end_row() const { return n - first_row() > (1 << r) ? first_row() + (1 << r) : n; }
   __device__ __forceinline__ int count() const { return tiles.count(s + first_row(), s + end_row() - 1); }
-  // The current unit's part in this range: tiles [off, off + the result) of its `all` own ones; 0: none (the range
-  // ends among what it counts for beside). x is then the part's first tile.
-  __device__ __forceinline__ int part(int& all) {
-    all = count();
+  // The current unit's part in this range; false: none (the range ends among what the unit counts for beside). x is
+  // then the part's first tile.
+  __device__ __forceinline__ bool part(ChunkPart& p) {
+    p.all = count();
     const int ahead = max(0, extra - off);
-    off = max(0, off - extra);
+    p.off = max(0, off - extra);
     x += ahead;
-    return max(0, min(all - off, end - x));
+    p.x = x;
+    p.m = min(p.all - p.off, end - x);
+    p.b = b;
+    p.s = s;
+    p.n = n;
+    p.c0 = c0;
+    p.row = first_row();
+    p.hg = hg;
+    return p.m > 0;
   }
   // On to the next unit, behind a part of m tiles; false: the range is at its end.
   __device__ __forceinline__ bool next(int m) {

@@ -241,7 +241,8 @@ chunk_f32_kernel(const float* __restrict__ Q, const float* __restrict__ Kp, cons
       ChunkWalk<6> walk;
       if (kind == 0 || (kind == 1 && !sp.pair_streams && open)) walk.begin(a, 0);
       else walk = place;
-      int m = 0, all = 0;
+      ChunkPart part;
+      part.m = 0;
       while (kind < 3) {
         bool more;
         if (open) {
@@ -255,31 +256,29 @@ chunk_f32_kernel(const float* __restrict__ Q, const float* __restrict__ Kp, cons
           if (walk.hg + 1 >= walk.HG && walk.t + 1 >= walk.units) walk.load(walk.group);   // (the lanes' sequences are not kept)
           more = walk.next(work.m);
         }
-        if (more) m = walk.part(all);
-        open = m == 0;
-        if (m > 0) break;
+        open = !(more && walk.part(part));
+        if (!open) break;
       }
       __syncwarp();
       if (lane == 0) {
         place = walk;
         work.kind = kind == 3 ? 0 : kind;
         if (kind < 3) {
-          const bool cut = m < all;
-          const int at = (int)blockIdx.x, second = walk.off == 0;
-          work.pos0 = walk.c0 + walk.first_row();
-          work.left = walk.n - walk.first_row();
-          work.h0 = kind == 1 ? walk.hg << sp.gp_shift : walk.hg * R;
+          const int at = (int)blockIdx.x, second = part.off == 0;
+          work.pos0 = part.c0 + part.row;
+          work.left = part.n - part.row;
+          work.h0 = kind == 1 ? part.hg << sp.gp_shift : part.hg * R;
           work.kvh = work.h0 / (a.Hq / a.Hkv);
-          work.b = walk.b;
-          work.s = walk.s;
-          work.end = walk.s + walk.n;
-          work.p0 = walk.s + walk.first_row();
-          work.off = walk.off;
-          work.m = m;
+          work.b = part.b;
+          work.s = part.s;
+          work.end = part.s + part.n;
+          work.p0 = part.s + part.row;
+          work.off = part.off;
+          work.m = part.m;
           work.skip = walk.tiles.skip(work.p0);
-          work.part = !cut ? -1 : (int)(kind == 1 ? sp.pair_part(at, second) : sp.single_part(at, second));
-          if (cut && second)
-            cuts[(kind == 1 ? 0 : sp.pair_streams) + at] = ChunkCut{work.pos0, work.left, work.h0, (walk.x + all - 1) / walk.range - at};
+          work.part = !part.cut() ? -1 : (int)(kind == 1 ? sp.pair_part(at, second) : sp.single_part(at, second));
+          if (part.cut() && second)
+            cuts[(kind == 1 ? 0 : sp.pair_streams) + at] = ChunkCut{work.pos0, work.left, work.h0, (part.x + part.all - 1) / walk.range - at};
         }
       }
     }

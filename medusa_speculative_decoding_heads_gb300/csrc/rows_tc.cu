@@ -67,6 +67,8 @@ constexpr int kSms = 152;
 constexpr int kLeastKeys = 256;   // of a key range that is one of several: two tiles
 // What a unit of new tokens over a paged cache counts for beside its key tiles.
 constexpr int kPairExtra = 2, kSingleExtra = 2;
+constexpr int kAlike = 4;   // single tiles whose key tiles differ by no more go side by side
+enum Dual : int { kDivided = 1, kApart = 2 };
 constexpr int kAhead = 8;   // steps (K and V tiles) of a unit still to be loaded when the next unit is fetched
 // The running maximum moves (and O is rescaled) only when a tile's maximum exceeds it by more
 // than this many binary orders of magnitude: weights stay below 2^8, far inside bf16 and f32.
@@ -374,9 +376,11 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
   if (kChunk && warp >= kPlanWarp) {
     // ------------------------------------------------------------------ schedule: ranges of the work
     // One range of the pairs' key tiles and one of the single tiles'; tile t's half of each unit by a warp for
-    // each t (both go through the same units). Both tiles of a pair take the same keys; a single tile's keys
-    // are divided between the two, so that there is one tile's softmax to hide behind the other's products, and
-    // joined at its end. (A range of its own for each tile leaves one idle where their units differ in length.)
+    // each t (both go through the same units). Both tiles of a pair take the same keys. Of single tiles two
+    // of like length go side by side (Unit::dual = kApart), so that there is one's softmax to hide behind
+    // the other's products; where the next one is of another length, a single tile's keys are divided between
+    // both and joined at its end (kDivided). (A range of its own for each tile leaves one idle where lengths differ:
+    // 24 single tokens 220 us.)
     const int t = warp - kPlanWarp;
     const ChunkSpace& sp = a.space;
     ChunkWalk<7> walk;
@@ -404,42 +408,63 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
       if (lane == 0 && t == 0) *cut_at = ChunkCut{0, 0, 0, 0};
       bool more = walk.open(single ? log_npos : log_npos + 1, single ? 1 : npos + 1, single ? npos : INT32_MAX,
                             single ? kSingleExtra : kPairExtra, (int)blockIdx.x, kSms);
-      while (more) {
-        int all;
-        const int m = walk.part(all);
-        if (m == 0) break;
-        if (!free_slot()) break;
+      auto publish = [&](const ChunkPart& own, const ChunkPart& other, int dual) {   // own: this warp's tile's
+        if (!free_slot()) return;
         Unit& d = units[i & 1];
-        const int row0 = walk.first_row() + (single ? 0 : t * npos), left = walk.n - row0;
-        const int skip = walk.tiles.skip(walk.s + walk.first_row()), half = (m + 1) >> 1;
-        const int j0 = single && t == 1 ? walk.off + half : walk.off;
-        const bool cut = m < all;   // (a unit that is cut writes partial results)
+        const int row0 = own.row + (single ? 0 : t * npos), left = own.n - row0;
+        const int skip = walk.tiles.skip(own.s + own.row), half = (own.m + 1) >> 1;
+        const int j0 = dual == kDivided && t == 1 ? own.off + half : own.off;
+        const int upto = dual == kDivided && t == 0 ? half : own.off + own.m - j0;
         if (lane == 0) {
           d.kind = kNew;
-          d.dual = single;
-          d.pos0[t] = walk.c0 + row0;
+          d.dual = dual;
+          d.pos0[t] = own.c0 + row0;
           d.left[t] = left;
-          d.h0[t] = walk.hg << a.gp_shift;
-          d.kvh[t] = (walk.hg << a.gp_shift) / (a.Hq / a.Hkv);
-          d.base[t] = walk.b;
-          d.k0[t] = walk.s;   // the sequence's first row, and one past its last
-          d.kend[t] = walk.s + walk.n;
+          d.h0[t] = own.hg << a.gp_shift;
+          d.kvh[t] = (own.hg << a.gp_shift) / (a.Hq / a.Hkv);
+          d.base[t] = own.b;
+          d.k0[t] = own.s;   // the sequence's first row, and one past its last
+          d.kend[t] = own.s + own.n;
           // (a pair's first tile may be through with its keys before the part begins)
-          const int own = left > 0 ? ((walk.s + row0 + min(left, npos) - 1) >> 7) + 1 - skip - walk.off : 0;
-          d.n[t] = single ? (t == 0 ? half : m - half) : max(0, min(m, own));
-          d.part[t] = !cut ? -1 : (int)(single ? sp.single_part(blockIdx.x, walk.off == 0) : sp.pair_part(blockIdx.x, walk.off == 0) + t * kRows);
-          d.p0[t] = walk.s + row0;
+          const int seen = left > 0 ? ((own.s + row0 + min(left, npos) - 1) >> 7) + 1 - skip - own.off : 0;
+          d.n[t] = single ? upto : max(0, min(own.m, seen));
+          d.part[t] = !own.cut() ? -1 : (int)(single ? sp.single_part(blockIdx.x, own.off == 0) : sp.pair_part(blockIdx.x, own.off == 0) + t * kRows);
+          d.p0[t] = own.s + row0;
           d.j0[t] = j0;
           d.skip[t] = skip;
-          if (cut && walk.off == 0 && t == 0)
-            *cut_at = ChunkCut{walk.c0 + row0, left, walk.hg << a.gp_shift, (walk.x + all - 1) / walk.range - (int)blockIdx.x};
+          auto note = [&](const ChunkPart& p) {
+            if (p.cut() && p.off == 0)
+              *cut_at = ChunkCut{p.c0 + p.row, p.n - p.row, p.hg << a.gp_shift, (p.x + p.all - 1) / walk.range - (int)blockIdx.x};
+          };
+          if (t == 0) {
+            note(own);
+            if (dual == kApart) note(other);
+          }
         }
-        if (j0 + lane < walk.off + m)
-          d.pages[t][lane] = a.table[(size_t)walk.b * a.max_pages + walk.tiles.tile(j0 + lane, skip) * kKeys / a.page_rows];
+        if (j0 + lane < own.off + own.m)
+          d.pages[t][lane] = a.table[(size_t)own.b * a.max_pages + walk.tiles.tile(j0 + lane, skip) * kKeys / a.page_rows];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&unit_full[i & 1]);
         ++i;
-        more = walk.next(m);
+      };
+      ChunkPart held, now;
+      bool have = false;
+      while (ok) {
+        bool got = more;
+        if (more) {
+          got = walk.part(now);
+          more = got && walk.next(now.m);
+        }
+        if (!single) {
+          if (!got) break;
+          publish(now, now, 0);
+          continue;
+        }
+        const bool apart = have && got && abs(held.m - now.m) <= kAlike;
+        if (have) publish(apart && t == 1 ? now : held, now, apart ? kApart : kDivided);
+        if (!have && !got) break;
+        have = got && !apart;
+        held = now;
       }
     }
     if (ok && free_slot()) {
@@ -601,7 +626,8 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
           const bool in_pool = page >= 0 && page < a.num_pages;
           MEDUSA_CHECK(isv || lane != 0 || in_pool, MEDUSA_CHECK_PAGE);
           // (what other rows of the sequence see stays: it is theirs that it holds numbers)
-          const int low = max(0, w.k0[0] - a.window + 1) - key0, first = a.sinks - key0, high = w.kend[0] - key0;
+          const int low = max(0, (t ? w.k0[1] : w.k0[0]) - a.window + 1) - key0, first = a.sinks - key0;
+          const int high = (t ? w.kend[1] : w.kend[0]) - key0;
           const bool fix = isv && (high < kKeys || (low > 0 && first < min(low, kKeys)));
           if (fix) {
             if (fix_wait) ok = until([&] { return !fix_wait; }, 16);
@@ -1018,7 +1044,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         tc::fence_after();
       }
       float w0 = 1.f, w1 = 0.f;   // chunks: what O_0 and O_1 are multiplied with
-      if (kChunk && single) {
+      if (kChunk && single == kDivided) {
         if (t == 1) {   // tile 0's warps take it from here
           back();       // (where this unit gave tile 1 no keys)
           if (!ok) break;
@@ -1058,7 +1084,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
       };
       if (!busy) {
-        if (kChunk && single) tc::mbar_arrive(&half_free);
+        if (kChunk && single == kDivided) tc::mbar_arrive(&half_free);
         continue;
       }
       // Four lanes hold four consecutive positions of one head. They trade 16-byte pieces, so that
@@ -1112,7 +1138,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
       }
       tc::fence_before();   // O has been read before the next unit's first P is announced
-      if (kChunk && single) tc::mbar_arrive(&half_free);
+      if (kChunk && single == kDivided) tc::mbar_arrive(&half_free);
     }
   }
 
