@@ -303,6 +303,12 @@ __device__ __forceinline__ Piece decode_prefix(const RowsArgs& a, int u, int t) 
   return w;
 }
 
+// Row and plane of a key tile in `page`; one outside the pool is past the planes, where TMA fills zeros.
+__device__ __forceinline__ int2 place_of(const RowsArgs& a, int key0, int page, int kvh) {
+  const bool in_pool = page >= 0 && page < a.num_pages;
+  return make_int2(key0 % a.page_rows, (in_pool ? page : a.num_pages) * a.Hkv + kvh);
+}
+
 template <int kD, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -534,11 +540,12 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     // In the MMA warp's order, as below. What has to wait for others is put off rather than waited for,
     // so that copies stay in flight: a tile of rows whose place is still in use, and the zeroing of what
     // no row of the sequence sees in a V tile that has not arrived. Both are looked after in every wait.
+    // (What stands between two copies counts: a page and a row worked out for each tile, 63 -> 60 us for 32
+    // tokens in a window.)
     ChunkTiles<7> list;
     list.begin(a.window, a.sinks);
-    Unit w;
-    int it = 0, nq[2] = {0, 0}, fixes = 0;   // ring position, Q tiles loaded, V tiles zeroed
-    int page_reg[2] = {-1, -1};
+    int st = 0, ph = 1, loaded = 0, fixes = 0;   // ring stage and phase of the next tile, tiles loaded, V tiles zeroed
+    int nq[2] = {0, 0};                          // Q tiles loaded
     bool ok = true, q_wait[2] = {false, false}, fix_wait = false;
     int q_pos[2] = {0, 0}, q_head[2] = {0, 0};
     int fix_stage = 0, fix_low = 0, fix_high = 0, fix_first = 0;   // rows [low, high) and those below first stay
@@ -577,7 +584,7 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     auto until = [&](auto done, uint32_t code) {
       const long long t0 = clock64();
       for (;;) {
-        serve();
+        if (q_wait[0] || q_wait[1] || fix_wait) serve();
         if (done()) return true;
         if (__any_sync(0xffffffffu, clock64() - t0 > 4000000000LL)) {
           if (lane == 0) atomicOr(err, code);
@@ -588,73 +595,85 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     for (int i = 0; ok; ++i) {
       ok = until([&] { return there(&unit_full[i & 1], (i >> 1) & 1); }, 1);
       if (!ok) break;
-      w = units[i & 1];
+      const Unit& u = units[i & 1];
+      const int kind = u.kind, dual = u.dual, n0 = u.n[0], n1 = u.n[1];
+      int2 place[2];   // of 32 tiles, one per lane
+      int j0[2], skip[2], b[2], kvh[2], end[2], low[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) page_reg[t] = units[i & 1].pages[t][lane];
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&unit_empty[i & 1]);
-      if (w.kind == kEnd) break;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (w.n[t] > 0) {
+      for (int t = 0; t < 2; ++t) {
+        j0[t] = u.j0[t];
+        skip[t] = u.skip[t];
+        b[t] = u.base[t];
+        kvh[t] = u.kvh[t];
+        place[t] = place_of(a, list.tile(j0[t] + lane, skip[t]) * kKeys, u.pages[t][lane], kvh[t]);
+        end[t] = u.kend[t];   // what no row of the sequence sees: from here on, and
+        low[t] = max(0, u.k0[t] - a.window + 1);   // below this, but for the first rows
+        if (kind != kEnd && (t ? n1 : n0) > 0) {
           if (q_wait[t]) ok = ok && until([&] { return !q_wait[t]; }, 4);
           q_wait[t] = true;
-          q_pos[t] = w.pos0[t];
-          q_head[t] = w.h0[t];
+          q_pos[t] = u.pos0[t];
+          q_head[t] = u.h0[t];
         }
-      const int nt = max(w.n[0], w.n[1]), tiles = w.dual ? 2 : 1;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&unit_empty[i & 1]);
+      if (kind == kEnd) break;
+      const int nt = max(n0, n1), tiles = dual ? 2 : 1;
 #pragma unroll 1
       for (int j = nt > 0 ? -1 : 0; ok && j < nt; ++j) {   // step j: V_j and K_{j+1}
 #pragma unroll 1
         for (int x = 0; ok && x < 2 * tiles; ++x) {
-          const int t = x >> 1, n = w.dual ? (t ? w.n[1] : w.n[0]) : nt, jt = j + (x & 1);
+          const int t = x >> 1, n = dual ? (t ? n1 : n0) : nt, jt = j + (x & 1);
           const bool isv = !(x & 1);
           if (jt < 0 || jt >= n) continue;
-          const int base = t ? w.base[1] : w.base[0], kvh = t ? w.kvh[1] : w.kvh[0];
-          const int skip = t ? w.skip[1] : w.skip[0], j0 = t ? w.j0[1] : w.j0[0];
-          const int st = it % kStages;
-          ok = until([&] { return it < kStages || there(&kv_empty[st], (it / kStages - 1) & 1); }, 8);
+          if (q_wait[0] || q_wait[1] || fix_wait) serve();
+          if (loaded >= kStages && !there(&kv_empty[st], ph)) ok = until([&] { return there(&kv_empty[st], ph); }, 8);
           if (!ok) break;
-          const int key0 = list.tile(j0 + jt, skip) * kKeys;
-          int pages = t ? page_reg[1] : page_reg[0];
-          if (!isv && (jt & 31) == 0 && jt > 0) {   // 32 tiles' pages at a time, one per lane (the first come with the unit)
-            pages = jt + lane < n ? a.table[(size_t)base * a.max_pages + list.tile(j0 + jt + lane, skip) * kKeys / a.page_rows] : -1;
-            if (t) page_reg[1] = pages;
-            else page_reg[0] = pages;
+          if (!isv && (jt & 31) == 0 && jt > 0) {   // 32 tiles' places at a time, one per lane (the first come with the unit)
+            const int key0 = list.tile((t ? j0[1] : j0[0]) + jt + lane, t ? skip[1] : skip[0]) * kKeys;
+            const int page = jt + lane < n ? a.table[(size_t)(t ? b[1] : b[0]) * a.max_pages + key0 / a.page_rows] : -1;
+            const int2 at = place_of(a, key0, page, t ? kvh[1] : kvh[0]);
+            if (t) place[1] = at;
+            else place[0] = at;
           }
-          const int page = __shfl_sync(0xffffffffu, pages, jt & 31);
-          const bool in_pool = page >= 0 && page < a.num_pages;
-          MEDUSA_CHECK(isv || lane != 0 || in_pool, MEDUSA_CHECK_PAGE);
-          // (what other rows of the sequence see stays: it is theirs that it holds numbers)
-          const int low = max(0, (t ? w.k0[1] : w.k0[0]) - a.window + 1) - key0, first = a.sinks - key0;
-          const int high = (t ? w.kend[1] : w.kend[0]) - key0;
-          const bool fix = isv && (high < kKeys || (low > 0 && first < min(low, kKeys)));
-          if (fix) {
-            if (fix_wait) ok = until([&] { return !fix_wait; }, 16);
-            if (!ok) break;
-            fix_wait = true;
-            fix_stage = st;
-            fix_low = low;
-            fix_high = high;
-            fix_first = first;
+          const int ty = __shfl_sync(0xffffffffu, t ? place[1].x : place[0].x, jt & 31);
+          const int tz = __shfl_sync(0xffffffffu, t ? place[1].y : place[0].y, jt & 31);
+          MEDUSA_CHECK(isv || lane != 0 || tz < a.num_pages * a.Hkv, MEDUSA_CHECK_PAGE);
+          bool fix = false;
+          if (isv) {   // (what other rows of the sequence see stays: it is theirs that it holds numbers)
+            const int key0 = list.tile((t ? j0[1] : j0[0]) + jt, t ? skip[1] : skip[0]) * kKeys;
+            const int below = (t ? low[1] : low[0]) - key0, first = a.sinks - key0, high = (t ? end[1] : end[0]) - key0;
+            fix = high < kKeys || (below > 0 && first < min(below, kKeys));
+            if (fix) {
+              if (fix_wait) ok = until([&] { return !fix_wait; }, 16);
+              if (!ok) break;
+              fix_wait = true;
+              fix_stage = st;
+              fix_low = below;
+              fix_high = high;
+              fix_first = first;
+            }
           }
           if (lane == 0) {
             uint8_t* dst = ring + st * kTile;
             uint64_t* bar = fix ? &tail : &kv_full[st];
-            const int y = key0 % a.page_rows, z = (in_pool ? page : a.num_pages) * a.Hkv + kvh;   // outside the pool: zeros
             tc::mbar_arrive_expect(bar, kTile);
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * kHalf, isv ? &tmV : &tmK, 64 * h, y, z, bar);
+            for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * kHalf, isv ? &tmV : &tmK, 64 * h, ty, tz, bar);
           }
           __syncwarp();
-          ++it;
+          ++loaded;
+          if (++st == kStages) {
+            st = 0;
+            ph ^= 1;
+          }
         }
       }
     }
     if (ok) until([&] { return !q_wait[0] && !q_wait[1] && !fix_wait; }, 16);
     // never leave with copies still landing in shared memory
     if (fix_wait) tc::mbar_wait(&tail, fixes & 1, err, 16);
-    for (int x = it > kStages ? it - kStages : 0; x < it; ++x)
+    for (int x = loaded > kStages ? loaded - kStages : 0; x < loaded; ++x)
       if (!(fix_wait && x % kStages == fix_stage)) tc::mbar_wait(&kv_full[x % kStages], (x / kStages) & 1, err, 32);
     for (int t = 0; t < 2; ++t)
       if (nq[t] > 0) tc::mbar_wait(&q_full[t], (nq[t] - 1) & 1, err, 64);
