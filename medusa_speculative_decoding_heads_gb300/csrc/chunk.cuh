@@ -87,21 +87,6 @@ struct ChunkWalk {
   int b, n, s, c0, t, units, hg, off;   // the current unit, and its first tile that is this stream's (extra ones first)
 
   __device__ __forceinline__ int lane() const { return threadIdx.x & 31; }
-  __device__ __forceinline__ void begin(const ChunkArgs& a, int gp_shift) {
-    tiles.begin(a.window, a.sinks);
-    cu = a.cu;
-    start = a.start;
-    B = a.B;
-    T = a.T;
-    L_cap = a.L_cap;
-    HG = a.Hq >> gp_shift;
-    if (B <= 32) return;
-    // the sequences from the first decrease of the offsets on have no rows
-#pragma unroll 4
-    for (int i = lane(); i < a.B; i += 32)
-      if (cu[i + 1] < cu[i]) B = min(B, i);
-    B = __reduce_min_sync(0xffffffffu, B);
-  }
   __device__ __forceinline__ bool mine() const { return my_n >= least && my_n <= most; }
   // The lanes' sequences; those that leave [0, T] or the cache have no rows.
   __device__ __forceinline__ void load(int g) {
@@ -120,6 +105,24 @@ struct ChunkWalk {
       my_s = f;
       my_c0 = a;
     }
+  }
+  __device__ __forceinline__ void begin(const ChunkArgs& a, int gp_shift) {
+    tiles.begin(a.window, a.sinks);
+    cu = a.cu;
+    start = a.start;
+    B = a.B;
+    T = a.T;
+    L_cap = a.L_cap;
+    HG = a.Hq >> gp_shift;
+    if (B <= 32) {   // (once for all; more are read again wherever they are looked at)
+      load(0);
+      return;
+    }
+    // the sequences from the first decrease of the offsets on have no rows
+#pragma unroll 4
+    for (int i = lane(); i < a.B; i += 32)
+      if (cu[i + 1] < cu[i]) B = min(B, i);
+    B = __reduce_min_sync(0xffffffffu, B);
   }
   __device__ __forceinline__ int units_of(int n_) const { return (int)(((unsigned)n_ + ((1u << r) - 1)) >> r); }
   // all heads' tiles of units number t_ of n_ rows from logical row s_ on
@@ -144,7 +147,8 @@ struct ChunkWalk {
     }
     return v;
   }
-  // The stream's range of the class's tiles and its first unit; false: it has none.
+  // The stream's range of the class's tiles and its first unit; false: it has none. (Little work is cut as thin as
+  // one tile: with four at least 333 rows behind 1000 in a window of 201 took 30 us instead of 24.)
   __device__ __forceinline__ bool open(int r_, int least_, int most_, int extra_, int stream, int streams) {
     r = r_;
     least = least_;
@@ -156,7 +160,7 @@ struct ChunkWalk {
       int y = x;
       for (int g = 0; g < B; g += 32) {
         if (pass == 0 || B > 32) {
-          load(g);
+          if (B > 32) load(g);
           const int m = mine() ? units_of(my_n) : 0;
           my_w = m == 1 ? all_heads(0, my_s, my_n) : 0;
           for (unsigned many = __ballot_sync(0xffffffffu, m > 1); many; many &= many - 1) {

@@ -249,11 +249,12 @@ chunk_f32_kernel(const float* __restrict__ Q, const float* __restrict__ Kp, cons
           ++kind;
           if (kind == 3) break;
           if (lane == 0) cuts[(kind == 1 ? 0 : sp.pair_streams) + blockIdx.x] = ChunkCut{0, 0, 0, 0};
+          if (walk.B <= 32) walk.load(0);
           walk.HG = kind == 1 ? a.Hq >> sp.gp_shift : a.Hq / R;
           more = walk.open(kind == 1 ? 31 - __clz(sp.npos) : 0, kind == 1 ? 2 : 1, kind == 1 ? INT32_MAX : 1,
                            kind == 1 ? kTileExtra : kTokenExtra, (int)blockIdx.x, kSms);
         } else {   // behind the unit that has just been worked on
-          if (walk.hg + 1 >= walk.HG && walk.t + 1 >= walk.units) walk.load(walk.group);   // (the lanes' sequences are not kept)
+          if (walk.hg + 1 >= walk.HG && walk.t + 1 >= walk.units) walk.load(walk.group);   // (what the lanes hold is not kept)
           more = walk.next(work.m);
         }
         open = !(more && walk.part(part));
