@@ -24,7 +24,7 @@
 namespace medusa {
 namespace {
 
-constexpr int kThreads = 128, kBlocks = 152 * 8;
+constexpr int kThreads = 128, kBlocks = 152 * 32, kFew = 152 * 64;   // kFew: heads of a call
 
 struct RotateArgs {
   const void *Q, *K, *qw, *kw;
@@ -229,7 +229,12 @@ cudaError_t launch_qk_norm_rotate(const medusa_cfg& c, const void* Q, const void
   a.R = rot_dim;
   a.pairs = pairing == MEDUSA_ROTATE_PAIRS;
   a.eps = eps;
-  return c.dtype == MEDUSA_F32 ? run<float, 4>(c, a, T, st) : run<uint16_t, 8>(c, a, T, st);
+  // Two heads to a group while the SMs hold all such groups at once (a shorter chain in each), more beyond, which
+  // share their angles: one token of 32/8 heads 2.3 us so and 3.4 with eight, 64 tokens of 40/40 2.8 and 3.7;
+  // 700 tokens 9.0 and 7.7, 8191 74 and 59.4 (four: 59.7).
+  const bool few = (int64_t)T * (c.Hq + c.Hkv) <= kFew;
+  if (c.dtype == MEDUSA_F32) return few ? run<float, 2>(c, a, T, st) : run<float, 4>(c, a, T, st);
+  return few ? run<uint16_t, 2>(c, a, T, st) : run<uint16_t, 8>(c, a, T, st);
 }
 
 }  // namespace medusa
