@@ -12,8 +12,11 @@ namespace {
 // Joins the partial results of the units that were cut: O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s. Eight
 // lanes to a row, each with its weights and D / 8 head dims, four of them next to each other in every 32. Bound by the
 // partial results' bytes, which lie in L2. (A warp to a row worked out where that is, and its weights, 32 times over:
-// 20 us behind 2048 rows after 14336, now 9.)
-constexpr int kMergeThreads = 256, kMergeLanes = 8, kMergeRows = kMergeThreads / kMergeLanes, kMergeParts = 4;
+// 20 us behind 2048 rows after 14336, now 12.6.)
+constexpr int kMergeThreads = 256, kMergeLanes = 8, kMergeRows = kMergeThreads / kMergeLanes;
+// Parts on their way at a time. In bf16 most rows have two or three (two: 12.6 us behind 2048 rows after 14336, four:
+// 16); in float32, where little work is cut into many, up to thirty (15 and 10.6 us for five sequences).
+template <typename T> constexpr int kMergeParts = sizeof(T) == 4 ? 4 : 2;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -25,7 +28,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads)
 chunk_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml_part, const ChunkCut* __restrict__ cuts,
                    const ChunkSpace sp, int Hq, T* __restrict__ O) {
-  constexpr int X = D / 32;
+  constexpr int X = D / 32, P = kMergeParts<T>;
   pdl_wait();
   pdl_trigger();
   // blocks: kMergeRows rows of each stream of pairs, then of single tiles
@@ -53,11 +56,11 @@ chunk_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m
   float4 acc[X];
 #pragma unroll
   for (int x = 0; x < X; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 <= cut.parts; s0 += kMergeParts) {
-    float2 ml[kMergeParts];
-    float4 o[kMergeParts][X];
+  for (int s0 = 0; s0 <= cut.parts; s0 += P) {
+    float2 ml[P];
+    float4 o[P][X];
 #pragma unroll
-    for (int i = 0; i < kMergeParts; ++i) {
+    for (int i = 0; i < P; ++i) {
       ml[i] = make_float2(-INFINITY, 0.f);
       if (s0 + i > cut.parts) continue;
       const int64_t at = place(s0 + i);
@@ -66,7 +69,7 @@ chunk_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m
       for (int x = 0; x < X; ++x) o[i][x] = *reinterpret_cast<const float4*>(o_part + at * D + 32 * x + 4 * sub);
     }
 #pragma unroll
-    for (int i = 0; i < kMergeParts; ++i) {
+    for (int i = 0; i < P; ++i) {
       if (ml[i].x == -INFINITY && ml[i].y == 0.f) continue;   // nothing was visible: its O need not have been written
       const float w = ex2(ml[i].x - mu);
       sum = fmaf(ml[i].y, w, sum);

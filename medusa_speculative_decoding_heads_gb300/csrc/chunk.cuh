@@ -88,24 +88,27 @@ struct ChunkWalk {
 
   __device__ __forceinline__ int lane() const { return threadIdx.x & 31; }
   __device__ __forceinline__ bool mine() const { return my_n >= least && my_n <= most; }
-  // The lanes' sequences; those that leave [0, T] or the cache have no rows.
-  __device__ __forceinline__ void load(int g) {
+  struct Bounds {
+    int first, end, start;
+  };
+  __device__ __forceinline__ Bounds fetch(int g) const {   // of sequence g + lane
     const int i = g + lane();
+    if (i >= B) return {0, 0, 0};
+    return {cu[i], cu[i + 1], start ? start[i] : 0};
+  }
+  // The lanes' sequences; those that leave [0, T] or the cache have no rows, nor have any from a decrease on.
+  __device__ __forceinline__ void settle(int g, const Bounds& q) {
     group = g;
     my_n = my_s = my_c0 = 0;
-    int a = 0, e = 0, f = 0;
-    if (i < B) {
-      a = cu[i];
-      e = cu[i + 1];
-      f = start ? start[i] : 0;
-    }
-    const unsigned falls = __ballot_sync(0xffffffffu, e < a);
-    if (!(falls & ((2u << lane()) - 1)) && a >= 0 && e > a && e <= T && f >= 0 && f <= L_cap - (e - a)) {
-      my_n = e - a;
-      my_s = f;
-      my_c0 = a;
+    const unsigned falls = __ballot_sync(0xffffffffu, q.end < q.first);
+    if (!(falls & ((2u << lane()) - 1)) && q.first >= 0 && q.end > q.first && q.end <= T && q.start >= 0 &&
+        q.start <= L_cap - (q.end - q.first)) {
+      my_n = q.end - q.first;
+      my_s = q.start;
+      my_c0 = q.first;
     }
   }
+  __device__ __forceinline__ void load(int g) { settle(g, fetch(g)); }
   __device__ __forceinline__ void begin(const ChunkArgs& a, int gp_shift) {
     tiles.begin(a.window, a.sinks);
     cu = a.cu;
@@ -114,15 +117,13 @@ struct ChunkWalk {
     T = a.T;
     L_cap = a.L_cap;
     HG = a.Hq >> gp_shift;
-    if (B <= 32) {   // (once for all; more are read again wherever they are looked at)
-      load(0);
-      return;
-    }
-    // the sequences from the first decrease of the offsets on have no rows
+    if (B > 32) {   // B becomes the number of those ahead of the first decrease of the offsets
 #pragma unroll 4
-    for (int i = lane(); i < a.B; i += 32)
-      if (cu[i + 1] < cu[i]) B = min(B, i);
-    B = __reduce_min_sync(0xffffffffu, B);
+      for (int i = lane(); i < a.B; i += 32)
+        if (cu[i + 1] < cu[i]) B = min(B, i);
+      B = __reduce_min_sync(0xffffffffu, B);
+    }
+    if (B <= 32) load(0);   // (once for all; more are read again wherever they are looked at)
   }
   __device__ __forceinline__ int units_of(int n_) const { return (int)(((unsigned)n_ + ((1u << r) - 1)) >> r); }
   // all heads' tiles of units number t_ of n_ rows from logical row s_ on
@@ -158,9 +159,18 @@ struct ChunkWalk {
     x = end = 0;
     for (int pass = 0;; ++pass) {   // the sum of all; then the sequence with tile x
       int y = x;
+      Bounds ahead[3];   // of the next groups: they arrive while one is worked on
+#pragma unroll
+      for (int k = 0; k < 3; ++k) ahead[k] = B > 32 ? fetch(32 * k) : Bounds{0, 0, 0};
+#pragma unroll 1
       for (int g = 0; g < B; g += 32) {
         if (pass == 0 || B > 32) {
-          if (B > 32) load(g);
+          if (B > 32) {
+            settle(g, ahead[0]);
+            ahead[0] = ahead[1];
+            ahead[1] = ahead[2];
+            ahead[2] = fetch(g + 96);
+          }
           const int m = mine() ? units_of(my_n) : 0;
           my_w = m == 1 ? all_heads(0, my_s, my_n) : 0;
           for (unsigned many = __ballot_sync(0xffffffffu, m > 1); many; many &= many - 1) {
@@ -172,11 +182,11 @@ struct ChunkWalk {
             if (lane() == from) my_w = w;
           }
         }
-        const int upto = scan(my_w), sum = __shfl_sync(0xffffffffu, upto, 31);
+        const int sum = __reduce_add_sync(0xffffffffu, my_w);
         if (pass == 0) {
           all += sum;
         } else if (y < sum) {
-          const int from = __ffs(__ballot_sync(0xffffffffu, upto > y)) - 1;
+          const int upto = scan(my_w), from = __ffs(__ballot_sync(0xffffffffu, upto > y)) - 1;
           y -= __shfl_sync(0xffffffffu, upto - my_w, from);
           take(from);
           break;

@@ -153,6 +153,31 @@ def test_many_sequences(B, dtype, D, Hq, Hkv):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,D", KINDS)
+@pytest.mark.parametrize("B,at", [(40, 3), (70, 31), (70, 32), (70, 33), (200, 150), (33, 0)])
+def test_many_sequences_ahead_of_a_decrease(B, at, dtype, D):
+    """Offsets that fall somewhere among more sequences than a warp has lanes: those ahead are right, none behind is computed."""
+    dev = gpu_ready()
+    c = Case([1 + b % 3 for b in range(B)], [(37 * b) % 300 for b in range(B)], 4, 2, D, dtype, dev, seed=B, pad=2)
+    cu = list(c.cu)
+    cu[at + 1] = cu[at] - 1
+    c.cu_d, c.cu = i32(cu, dev), cu
+    c.check(c.call(), f"{at} of {B}")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (F32, 64)])
+def test_thousands_of_sequences(dtype, D):
+    """Single tokens and a few longer ones among 3000 sequences; finding whose work is whose stays cheap beside it."""
+    dev = gpu_ready()
+    B = 3000
+    rows = [1] * B
+    rows[17], rows[1500], rows[2999], rows[40] = 300, 2, 150, 0
+    c = Case(rows, [b % 140 for b in range(B)], 2, 1, D, dtype, dev, seed=1)
+    c.check(c.call())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,D", KINDS)
 def test_no_start_is_zero(dtype, D):
     """A prompt in one piece: start may be NULL, and the rows are those of medusa_prompt_attention's formula."""
     dev = gpu_ready()
