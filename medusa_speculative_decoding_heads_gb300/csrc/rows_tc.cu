@@ -565,13 +565,20 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
       if (fix_wait && there(&tail, fixes & 1)) {
         uint8_t* dst = ring + fix_stage * kTile;
+        auto zero = [&](int from, int to) {   // rows [from, to)
 #pragma unroll 1
-        for (int c = lane; c < kKeys * 8; c += 32) {
-          const int row = c >> 3;
-          if (row < fix_high && (row >= fix_low || row < fix_first)) continue;
+          for (int c0 = 8 * from + lane; c0 < 8 * to; c0 += 128) {
 #pragma unroll
-          for (int h = 0; h < kHalves; ++h) reinterpret_cast<uint4*>(dst + h * kHalf)[c] = make_uint4(0, 0, 0, 0);
-        }
+            for (int c = c0; c < c0 + 128; c += 32)
+              if (c < 8 * to) {
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) reinterpret_cast<uint4*>(dst + h * kHalf)[c] = make_uint4(0, 0, 0, 0);
+              }
+          }
+        };
+        // (the bounds count from the tile on and may lie far off it)
+        zero(max(0, min(kKeys, fix_high)), kKeys);
+        zero(max(0, fix_first), max(0, min(kKeys, min(fix_low, fix_high))));
         tc::fence_proxy_async();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&kv_full[fix_stage]);
