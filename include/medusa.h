@@ -526,7 +526,7 @@ MEDUSA_API int medusa_pages_compact(const medusa_cfg* cfg, void* Kp, void* Vp, i
                                     int32_t* page_map, int32_t* n_live, void* workspace, medusa_stream_t stream);
 
 /* Failure detection. Every spin-wait of the tcgen05 kernels (the heads GEMVs, and
- * tree, prompt and prefix attention, which share the attention word: pipeline
+ * tree, prompt, prefix and chunk attention, which share the attention word: pipeline
  * mbarriers, the softmax exchanges) is bounded by a clock budget of about two
  * seconds. (That covers waits, not an instruction that itself does not complete.)
  * On expiry the waiting thread ORs a code

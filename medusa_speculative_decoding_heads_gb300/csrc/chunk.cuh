@@ -3,8 +3,8 @@
 // Work. A unit is a block of query rows (the query heads of one KV head that share a tile, times
 // positions) of one sequence; it takes the key tiles that any of its rows sees, the first rows' ones
 // ahead of the window's. All units' tiles, one after another, are cut into equal ranges, one for each
-// stream (a CTA), wherever the cuts fall: lengths differ from
-// sequence to sequence and are on the device only, and so are the cuts. A unit that is cut leaves partial
+// stream (a CTA), wherever the cuts fall: lengths differ from sequence to sequence and are on the device
+// only, and so are the cuts. A unit that is cut leaves partial
 // results, at most two per stream (of the unit that was begun ahead of its range, and of the one that
 // ends behind it), which chunk_merge_kernel joins.
 #pragma once

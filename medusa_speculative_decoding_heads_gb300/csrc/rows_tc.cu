@@ -1,6 +1,7 @@
 // Attention of packed query rows on 5th-generation tensor cores (tcgen05, TMEM
-// accumulators, TMA), bf16: whole prompts (causal; D = 64 or 128), and tree attention
-// behind a prefix that the batch shares (D = 128).
+// accumulators, TMA), bf16: whole prompts (causal; D = 64 or 128), tree attention
+// behind a prefix that the batch shares (D = 128), and new tokens over the pages of a cache,
+// with or without a window (D = 64 or 128).
 //
 // O = softmax(Q K^T / sqrt(D)) V in one pass over the keys, with the running maximum and
 // sum of "최적화 2편" (beengineer500), section 3.3. 4 rows keys D operations against
@@ -29,6 +30,11 @@
 //   warp 10         the schedule: a unit per block of the grid, longest first; this warp takes over
 //                   blocks that have not started (cluster launch control) and decodes the next
 //                   unit while the others work on this one.
+// New tokens over a paged cache (kChunkMode) differ in the schedule, in where K and V lie and in masks: one
+// CTA per SM has its range of all key tiles (chunk.cuh), which warps 10 and 11 follow, a tile's half each; warp 9
+// puts off what it would have to wait for. 2048 rows after 14336, 32/8 heads: 308 us alone between pauses (1670
+// TFLOP/s, 0.87 of the measured cuBLAS burst), 340 with the merge in a loop under the power limit; 32 single tokens
+// of 4096 to 16384 rows 194 us (6.7 TB/s, 0.98 of the measured copy).
 // TMEM: S_0, S_1, O_0, O_1 (128 columns each; O uses D of them). Every mbarrier wait is bounded.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -65,7 +71,9 @@ constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSms = 152;
 constexpr int kLeastKeys = 256;   // of a key range that is one of several: two tiles
-// What a unit of new tokens over a paged cache counts for beside its key tiles.
+// What a unit of new tokens over a paged cache counts for beside its key tiles: Q, the pipeline's filling and
+// its epilogue. (Nothing: 24 single tokens of 1 to 4000 rows, 40 heads, 235 us, so 136; 2048 rows of a prompt 78 and
+// 57. Pairs 4: 8192 rows in a window of 1024 169 us, 2: 163; singles 4: mixed step 59.7 us, 2: 58.4.)
 constexpr int kPairExtra = 2, kSingleExtra = 2;
 constexpr int kAlike = 4;   // single tiles whose key tiles differ by no more go side by side
 enum Dual : int { kDivided = 1, kApart = 2 };
@@ -540,8 +548,9 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     // In the MMA warp's order, as below. What has to wait for others is put off rather than waited for,
     // so that copies stay in flight: a tile of rows whose place is still in use, and the zeroing of what
     // no row of the sequence sees in a V tile that has not arrived. Both are looked after in every wait.
-    // (What stands between two copies counts: a page and a row worked out for each tile, 63 -> 60 us for 32
-    // tokens in a window.)
+    // (What stands between two copies counts: with page and row worked out for each tile 8192 rows in a window
+    // took 171 us, now 163; with boxes of 32 rows for tiles that are not seen whole, which load less, 40 tokens of one
+    // row each 51 us instead of 46.)
     ChunkTiles<7> list;
     list.begin(a.window, a.sinks);
     int st = 0, ph = 1, loaded = 0, fixes = 0;   // ring stage and phase of the next tile, tiles loaded, V tiles zeroed
