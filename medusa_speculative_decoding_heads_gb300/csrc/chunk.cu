@@ -14,9 +14,11 @@ namespace {
 // partial results' bytes, which lie in L2. (A warp to a row worked out where that is, and its weights, 32 times over:
 // 20 us behind 2048 rows after 14336, now 12.6.)
 constexpr int kMergeThreads = 256, kMergeLanes = 8, kMergeRows = kMergeThreads / kMergeLanes;
+constexpr int kMergeSplit = 4;   // groups of lanes to a row of a single tile, whose parts they divide: there are few rows, of many parts
+constexpr int kMergeBlocks = 2;
 // Parts on their way at a time. In bf16 most rows have two or three (two: 12.6 us behind 2048 rows after 14336, four:
-// 16); in float32, where little work is cut into many, up to thirty (15 and 10.6 us for five sequences).
-template <typename T> constexpr int kMergeParts = sizeof(T) == 4 ? 4 : 2;
+// 16); in float32, where little work is cut into many, up to thirty (D = 64: 15 and 10.6 us for five sequences).
+template <typename T, int D> constexpr int kMergeParts = sizeof(T) == 4 && D == 64 ? 4 : 2;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -24,46 +26,41 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Row i of a cut: its parts turn, turn + step, ... by eight lanes, or by the four groups of eight of a warp.
 template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads)
-chunk_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml_part, const ChunkCut* __restrict__ cuts,
-                   const ChunkSpace sp, int Hq, T* __restrict__ O) {
-  constexpr int X = D / 32, P = kMergeParts<T>;
-  pdl_wait();
-  pdl_trigger();
-  // blocks: kMergeRows rows of each stream of pairs, then of single tiles
-  const int per_pair = sp.pair_rows / kMergeRows, per_single = (sp.single_rows + kMergeRows - 1) / kMergeRows;
-  const bool pair = (int)blockIdx.x < sp.pair_streams * per_pair;
-  const int y = pair ? (int)blockIdx.x : (int)blockIdx.x - sp.pair_streams * per_pair, per = pair ? per_pair : per_single;
-  const int stream = y / per, sub = threadIdx.x % kMergeLanes;
-  const int r = (y - stream * per) * kMergeRows + threadIdx.x / kMergeLanes;
-  const ChunkCut cut = cuts[(pair ? 0 : sp.pair_streams) + stream];
-  if (cut.parts == 0 || r >= (pair ? sp.pair_rows : sp.single_rows)) return;
-  const int along = pair ? sp.npos : sp.single_npos, tile_rows = along << sp.gp_shift;   // rows of a tile: [head][position]
-  const int tile = r >= tile_rows, in_tile = r - tile * tile_rows, head = in_tile / along, pos = in_tile - head * along + tile * along;
+__device__ __forceinline__ void join(const float* __restrict__ o_part, const float* __restrict__ ml_part, const ChunkSpace& sp,
+                                     const ChunkCut& cut, bool pair, int stream, int i, int turn, int step, int sub, int Hq,
+                                     T* __restrict__ O) {
+  constexpr int X = D / 32, P = kMergeParts<T, D>;
+  // rows of a tile lie [head][position]
+  const int along = pair ? sp.npos : sp.single_npos, tile_rows = along << sp.gp_shift;
+  const int tile = pair && i >= tile_rows, in_tile = i - tile * tile_rows;
+  const int head = in_tile / (pair ? along : cut.left), at_pos = in_tile - head * (pair ? along : cut.left), pos = at_pos + tile * along;
+  const int r = pair ? i : head * along + at_pos;
   if (pos >= cut.left) return;
   const int64_t rows = pair ? sp.pair_rows : sp.single_rows;
   // part 0 is the stream's second one, the others are the first ones of those behind it
   const int64_t at0 = (pair ? sp.pair_part(stream, 1) : sp.single_part(stream, 1)) + r;
   auto place = [&](int s) { return s == 0 ? at0 : at0 + (2 * s - 1) * rows; };
-  float M = -INFINITY;   // (a row's lanes take the parts in turn)
-  for (int s = sub; s <= cut.parts; s += kMergeLanes) M = fmaxf(M, ml_part[2 * place(s)]);
-  const unsigned lanes = ((1u << kMergeLanes) - 1) << (threadIdx.x & 31) / kMergeLanes * kMergeLanes;
-#pragma unroll
-  for (int o = kMergeLanes / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, o));
+  // a row's lanes, which are here together: eight of them, or a whole warp
+  const int wide = kMergeLanes * step;
+  const unsigned lanes = pair ? ((1u << kMergeLanes) - 1) << (threadIdx.x & 31) / kMergeLanes * kMergeLanes : 0xffffffffu;
+  float M = -INFINITY;   // (they take the parts in turn)
+  for (int s = turn * kMergeLanes + sub; s <= cut.parts; s += wide) M = fmaxf(M, ml_part[2 * place(s)]);
+  for (int o = wide / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, o));
   const float mu = M == -INFINITY ? 0.f : M;
   float sum = 0.f;
   float4 acc[X];
 #pragma unroll
   for (int x = 0; x < X; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 <= cut.parts; s0 += P) {
+  for (int s0 = turn; s0 <= cut.parts; s0 += P * step) {
     float2 ml[P];
     float4 o[P][X];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       ml[i] = make_float2(-INFINITY, 0.f);
-      if (s0 + i > cut.parts) continue;
-      const int64_t at = place(s0 + i);
+      if (s0 + i * step > cut.parts) continue;
+      const int64_t at = place(s0 + i * step);
       ml[i] = *reinterpret_cast<const float2*>(ml_part + 2 * at);
 #pragma unroll
       for (int x = 0; x < X; ++x) o[i][x] = *reinterpret_cast<const float4*>(o_part + at * D + 32 * x + 4 * sub);
@@ -79,6 +76,20 @@ chunk_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m
         acc[x] = make_float4(fmaf(v.x, w, acc[x].x), fmaf(v.y, w, acc[x].y), fmaf(v.z, w, acc[x].z), fmaf(v.w, w, acc[x].w));
       }
     }
+  }
+  if (!pair) {
+#pragma unroll
+    for (int o = kMergeLanes; o < 32; o <<= 1) {
+      sum += __shfl_xor_sync(lanes, sum, o);
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        acc[x].x += __shfl_xor_sync(lanes, acc[x].x, o);
+        acc[x].y += __shfl_xor_sync(lanes, acc[x].y, o);
+        acc[x].z += __shfl_xor_sync(lanes, acc[x].z, o);
+        acc[x].w += __shfl_xor_sync(lanes, acc[x].w, o);
+      }
+    }
+    if (turn) return;
   }
   const float inv = 1.f / sum;   // (0 where every visible score is -inf: no number)
   T* op = O + ((size_t)(cut.pos0 + pos) * Hq + cut.h0 + head) * D + 4 * sub;
@@ -97,8 +108,30 @@ chunk_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ m
 }
 
 template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads)
+chunk_merge_kernel(const float* __restrict__ o_part, const float* __restrict__ ml_part, const ChunkCut* __restrict__ cuts,
+                   const ChunkSpace sp, int Hq, T* __restrict__ O) {
+  static_assert(kMergeLanes * kMergeSplit == 32, "a row of a single tile is a warp's");
+  pdl_wait();
+  pdl_trigger();
+  // blocks: kMergeRows rows of each stream of pairs; then kMergeBlocks for each stream of single tiles, which go
+  // through the rows that its cut has (most have few: a block for every eight that there may be took 2 us more)
+  const int per_pair = sp.pair_rows / kMergeRows;
+  const bool pair = (int)blockIdx.x < sp.pair_streams * per_pair;
+  const int y = pair ? (int)blockIdx.x : (int)blockIdx.x - sp.pair_streams * per_pair, per = pair ? per_pair : kMergeBlocks;
+  const int stream = y / per, sub = threadIdx.x % kMergeLanes, step = pair ? 1 : kMergeSplit;
+  const int slot = (y - stream * per) * kMergeRows + threadIdx.x / kMergeLanes;
+  const int turn = pair ? 0 : slot % kMergeSplit;   // the row's parts turn, turn + step, ... are this group's
+  const ChunkCut cut = cuts[(pair ? 0 : sp.pair_streams) + stream];
+  if (cut.parts == 0) return;
+  const int count = pair ? sp.pair_rows : cut.left << sp.single_shift;
+  for (int i = pair ? slot : slot / kMergeSplit; i < count; i += pair ? count : kMergeBlocks * kMergeRows / kMergeSplit)
+    join<T, D>(o_part, ml_part, sp, cut, pair, stream, i, turn, step, sub, Hq, O);
+}
+
+template <typename T, int D>
 cudaError_t merge(const medusa_cfg& c, void* O, const ChunkSpace& sp, void* ws, cudaStream_t st) {
-  const int blocks = sp.pair_streams * (sp.pair_rows / kMergeRows) + sp.streams * ((sp.single_rows + kMergeRows - 1) / kMergeRows);
+  const int blocks = sp.pair_streams * (sp.pair_rows / kMergeRows) + sp.streams * kMergeBlocks;
   const char* base = static_cast<const char*>(ws);
   const cudaError_t e = launch_pdl(chunk_merge_kernel<T, D>, blocks, kMergeThreads, 0, st, reinterpret_cast<const float*>(base),
                                    reinterpret_cast<const float*>(base + sp.ml), reinterpret_cast<const ChunkCut*>(base + sp.cuts), sp,
@@ -121,7 +154,8 @@ ChunkSpace chunk_space(const medusa_cfg& c, int T) {
   sp.pair_rows = f32 ? rows : 2 * rows;
   sp.streams = kChunkStreams;
   sp.single_npos = f32 ? 1 : T < sp.npos ? T : sp.npos;
-  sp.single_rows = f32 ? 1 << (sp.gp_shift < 2 ? sp.gp_shift : 2) : sp.single_npos << sp.gp_shift;
+  sp.single_shift = f32 && sp.gp_shift > 2 ? 2 : sp.gp_shift;
+  sp.single_rows = sp.single_npos << sp.single_shift;
   const size_t all = (size_t)2 * sp.pair_streams * sp.pair_rows + (size_t)2 * sp.streams * sp.single_rows;
   sp.ml = align_up(all * c.D * 4, 256);
   sp.cuts = sp.ml + align_up(all * 8, 256);

@@ -41,7 +41,7 @@ struct ChunkCut {
 struct ChunkSpace {
   int gp_shift, npos;          // query heads of a tile (log2), positions of a tile
   int pair_streams, pair_rows; // streams, and rows of one partial result
-  int streams, single_rows, single_npos;   // the same of single tiles, and their positions
+  int streams, single_rows, single_npos, single_shift;   // the same of single tiles, their positions and heads (log2)
   size_t ml, cuts, total;      // where maxima and sums begin, and the cuts, in bytes
   __host__ __device__ int64_t pair_part(int stream, int second) const { return ((int64_t)2 * stream + second) * pair_rows; }
   __host__ __device__ int64_t single_part(int stream, int second) const {

@@ -6,8 +6,8 @@
 //   single tokens                    up to 4 query heads of a KV head; a warp (D = 64: half of one) reads a key's
 //                                    row at a time, 4 of them on their way while 4 are worked on, and the
 //                                    warps join at the end of the unit: bound by the K/V bytes
-// 1500 rows of a prompt, 8 heads of 64: 85 us (whole prompts: 77); 8 single tokens of 2000 rows, 40 heads of 128:
-// 145 us (4.5 TB/s); 24 of 4000 rows, 32/8 heads: 225 us (3.5 TB/s: four rows' sums over 32 lanes).
+// 1500 rows of a prompt, 8 heads of 64: 87 us (whole prompts: 77); 8 single tokens of 2000 rows, 40 heads of 128:
+// 148 us (4.4 TB/s); 24 of 4000 rows, 32/8 heads: 222 us (3.5 TB/s: four rows' sums over 32 lanes).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -223,72 +223,79 @@ __device__ __forceinline__ void token_unit(float* smem, const float* __restrict_
   if (w.part >= 0 && lane == 0) *reinterpret_cast<float2*>(ml_part + 2 * (size_t)(w.part + warp)) = make_float2(M, sum);
 }
 
+// Warp 0 finds the next unit: `work` becomes it. kind: what was worked on last (0: nothing yet, 1: 64 rows, 2: single
+// tokens). A function of its own, as what it keeps in registers is not for the others to go without (in line: 24 single
+// tokens of 2000 rows, 8/4 heads of 64, 43 us, so 38; 8 of 2000 rows, 40 heads of 128, 167 and 148).
+template <int R>
+__device__ __noinline__ void find_work(const ChunkArgs& a, const ChunkSpace& sp, ChunkWalk<6>& place, Work& work, ChunkCut* cuts, int kind) {
+  const int lane = threadIdx.x & 31;
+  ChunkWalk<6> walk;
+  bool open = kind == 0;
+  if (open) {
+    walk.begin(a, 0);
+    kind = sp.pair_streams ? 0 : 1;
+  } else {
+    walk = place;
+  }
+  ChunkPart part;
+  part.m = 0;
+  while (kind < 3) {
+    bool more;
+    if (open) {
+      ++kind;
+      if (kind == 3) break;
+      if (lane == 0) cuts[(kind == 1 ? 0 : sp.pair_streams) + blockIdx.x] = ChunkCut{0, 0, 0, 0};
+      if (walk.B <= 32) walk.load(0);
+      walk.HG = kind == 1 ? a.Hq >> sp.gp_shift : a.Hq / R;
+      more = walk.open(kind == 1 ? 31 - __clz(sp.npos) : 0, kind == 1 ? 2 : 1, kind == 1 ? INT32_MAX : 1,
+                       kind == 1 ? kTileExtra : kTokenExtra, (int)blockIdx.x, kSms);
+    } else {   // behind the unit that has just been worked on
+      if (walk.hg + 1 >= walk.HG && walk.t + 1 >= walk.units) walk.load(walk.group);   // (what the lanes hold is not kept)
+      more = walk.next(work.m);
+    }
+    open = !(more && walk.part(part));
+    if (!open) break;
+  }
+  __syncwarp();
+  if (lane != 0) return;
+  place = walk;
+  work.kind = kind == 3 ? 0 : kind;
+  if (kind == 3) return;
+  const int at = (int)blockIdx.x, second = part.off == 0;
+  work.pos0 = part.c0 + part.row;
+  work.left = part.n - part.row;
+  work.h0 = kind == 1 ? part.hg << sp.gp_shift : part.hg * R;
+  work.kvh = work.h0 / (a.Hq / a.Hkv);
+  work.b = part.b;
+  work.s = part.s;
+  work.end = part.s + part.n;
+  work.p0 = part.s + part.row;
+  work.off = part.off;
+  work.m = part.m;
+  work.skip = walk.tiles.skip(work.p0);
+  work.part = !part.cut() ? -1 : (int)(kind == 1 ? sp.pair_part(at, second) : sp.single_part(at, second));
+  if (part.cut() && second)
+    cuts[(kind == 1 ? 0 : sp.pair_streams) + at] = ChunkCut{work.pos0, work.left, work.h0, (part.x + part.all - 1) / walk.range - at};
+}
+
 template <int D, int R>
 __global__ void __launch_bounds__(Smem<D>::threads, 1)
 chunk_f32_kernel(const float* __restrict__ Q, const float* __restrict__ Kp, const float* __restrict__ Vp, float* __restrict__ O,
-                 const ChunkArgs a, const ChunkSpace sp, float* __restrict__ o_part, float* __restrict__ ml_part, ChunkCut* cuts) {
+                 const __grid_constant__ ChunkArgs a, const __grid_constant__ ChunkSpace sp, float* __restrict__ o_part,
+                 float* __restrict__ ml_part, ChunkCut* cuts) {
   extern __shared__ __align__(16) float smem[];
   __shared__ Work work;
   __shared__ ChunkWalk<6> place;
-  const int lane = threadIdx.x & 31;
   pdl_trigger();   // (one CTA per SM, as many as there are, leaves nothing to crowd)
   pdl_wait();
   ChunkTiles<6> tiles;
   tiles.begin(a.window, a.sinks);
   const Cache cache{a, Kp, Vp, D};
-  int kind = sp.pair_streams ? 0 : 1;   // 1: 64 rows, 2: single tokens, once opened
-  bool open = true;
-  for (;;) {
-    if (threadIdx.x < 32) {   // warp 0 finds the next unit
-      ChunkWalk<6> walk;
-      if (kind == 0 || (kind == 1 && !sp.pair_streams && open)) walk.begin(a, 0);
-      else walk = place;
-      ChunkPart part;
-      part.m = 0;
-      while (kind < 3) {
-        bool more;
-        if (open) {
-          ++kind;
-          if (kind == 3) break;
-          if (lane == 0) cuts[(kind == 1 ? 0 : sp.pair_streams) + blockIdx.x] = ChunkCut{0, 0, 0, 0};
-          if (walk.B <= 32) walk.load(0);
-          walk.HG = kind == 1 ? a.Hq >> sp.gp_shift : a.Hq / R;
-          more = walk.open(kind == 1 ? 31 - __clz(sp.npos) : 0, kind == 1 ? 2 : 1, kind == 1 ? INT32_MAX : 1,
-                           kind == 1 ? kTileExtra : kTokenExtra, (int)blockIdx.x, kSms);
-        } else {   // behind the unit that has just been worked on
-          if (walk.hg + 1 >= walk.HG && walk.t + 1 >= walk.units) walk.load(walk.group);   // (what the lanes hold is not kept)
-          more = walk.next(work.m);
-        }
-        open = !(more && walk.part(part));
-        if (!open) break;
-      }
-      __syncwarp();
-      if (lane == 0) {
-        place = walk;
-        work.kind = kind == 3 ? 0 : kind;
-        if (kind < 3) {
-          const int at = (int)blockIdx.x, second = part.off == 0;
-          work.pos0 = part.c0 + part.row;
-          work.left = part.n - part.row;
-          work.h0 = kind == 1 ? part.hg << sp.gp_shift : part.hg * R;
-          work.kvh = work.h0 / (a.Hq / a.Hkv);
-          work.b = part.b;
-          work.s = part.s;
-          work.end = part.s + part.n;
-          work.p0 = part.s + part.row;
-          work.off = part.off;
-          work.m = part.m;
-          work.skip = walk.tiles.skip(work.p0);
-          work.part = !part.cut() ? -1 : (int)(kind == 1 ? sp.pair_part(at, second) : sp.single_part(at, second));
-          if (part.cut() && second)
-            cuts[(kind == 1 ? 0 : sp.pair_streams) + at] = ChunkCut{work.pos0, work.left, work.h0, (part.x + part.all - 1) / walk.range - at};
-        }
-      }
-    }
+  for (int kind = 0;;) {
+    if (threadIdx.x < 32) find_work<R>(a, sp, place, work, cuts, kind);
     __syncthreads();
     kind = work.kind;
     if (kind == 0) return;
-    open = false;
     if (kind == 1) tile_unit<D>(smem, Q, cache, tiles, sp, work, O, o_part, ml_part);
     else token_unit<D, R>(smem, Q, cache, tiles, work, O, o_part, ml_part);
     __syncthreads();   // the next unit goes where this one was
