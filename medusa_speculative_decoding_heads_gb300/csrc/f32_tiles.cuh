@@ -1,5 +1,6 @@
-// Attention of 64 query rows against tiles of 64 keys in float32 on the CUDA cores: what the kernels of
-// whole prompts and of new tokens over a paged cache share (prompt_f32.cu has the figures).
+// Attention of 64 query rows against tiles of 64 keys in float32 on the CUDA cores, for new tokens over a paged cache.
+// The layout is that of whole prompts (prompt_f32.cu, which has its reasons and figures, and keeps code of
+// its own: on these functions 8192 tokens, 8 heads of 64, took 1409 us instead of 1374).
 #pragma once
 
 #include <cuda_runtime.h>

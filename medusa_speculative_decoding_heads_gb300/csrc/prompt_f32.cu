@@ -22,7 +22,6 @@
 #include <stdint.h>
 
 #include "common.cuh"
-#include "f32_tiles.cuh"
 #include "prompt_walk.cuh"
 
 namespace medusa {
@@ -33,7 +32,30 @@ namespace {
 // them 3865 and 1541 (two CTAs per SM 185 and 1493); 128 of them and one of 4000 rows 403 and 399
 // (409), but 64 with one of 4000 373 and 385.
 constexpr int kManyPrompts = 64, kManyGrid = 4 * 152;
-using namespace f32;
+constexpr int kTileShift = 6, kTileRows = 1 << kTileShift, kTileKeys = 64, kGroup = 128;
+
+template <int D>
+struct Smem {
+  static constexpr int groups = D == 64 ? 3 : 2;
+  static constexpr int threads = groups * kGroup;
+  static constexpr int ld = D + 4;            // padded row of Q and K (floats)
+  static constexpr int ldp = kTileKeys + 8;   // padded row of P
+  static constexpr int k = kTileRows * ld;    // behind Q: K, V and P of each group
+  static constexpr int v = k + kTileKeys * ld;
+  static constexpr int p = v + kTileKeys * D;
+  static constexpr int per_group = p + kTileRows * ldp - k;
+  static constexpr int bytes = (k + groups * per_group) * 4;
+  static_assert(kTileRows * (D + 2) <= per_group, "a group's result must fit its tiles");
+  static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+};
+
+__device__ __forceinline__ void cp16(float* dst, const float* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(valid ? 16 : 0));
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N)); }
 
 // 64 rows of `stride` floats from src into rows of ld floats, by thread `tid` of `threads`; rows
 // past `live` become zeros.
@@ -54,50 +76,173 @@ __device__ __forceinline__ void prompt_unit(float* smem, const float* __restrict
                                             const int32_t* __restrict__ cu, int Hq, int Hkv, float scale_log2,
                                             float* __restrict__ O, int b, int r0, int h) {
   using S = Smem<D>;
-  Rows<D> t;
-  t.begin(smem);
-  const int group = t.group, tid = t.tid;
+  constexpr int NC = D / 32;   // 4-column groups of O per thread, 32 columns apart
+  const int group = threadIdx.x / kGroup, tid = threadIdx.x % kGroup;
+  float *sq = smem, *sk = smem + S::k + group * S::per_group, *sv = sk + S::v - S::k, *sp = sk + S::p - S::k;
+  const int rg = (tid >> 5) * 16 + ((tid & 1) | ((tid >> 3) & 2)), cg = (tid >> 1) & 7;   // rows rg + 4 i, keys cg + 8 c, head dims 4 cg + 32 n ..
+  auto sync_group = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroup) : "memory"); };
   const int kvh = h / (Hq / Hkv);
   const int64_t c0 = cu[b];
   const int len = cu[b + 1] - (int)c0, rows = min(kTileRows, len - r0), keys = r0 + rows;
   const int nt = (keys + kTileKeys - 1) / kTileKeys;
   const float* kp = K + c0 * ks + (size_t)kvh * D;
   const float* vp = V + c0 * vs + (size_t)kvh * D;
-  load_tile<D>(t.sq, S::ld, Q + (c0 + r0) * qs + (size_t)h * D, qs, rows, threadIdx.x, S::threads);
-  if (group < nt) load_tile<D>(t.sk, S::ld, kp + (int64_t)group * kTileKeys * ks, ks, keys - group * kTileKeys, tid, kGroup);
+  load_tile<D>(sq, S::ld, Q + (c0 + r0) * qs + (size_t)h * D, qs, rows, threadIdx.x, S::threads);
+  if (group < nt) load_tile<D>(sk, S::ld, kp + (int64_t)group * kTileKeys * ks, ks, keys - group * kTileKeys, tid, kGroup);
   cp_commit();
+
+  float4 o[4][NC];
+  float m[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) o[i][n] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   cp_wait<0>();
   __syncthreads();       // Q
   for (int j = group; j < nt; j += S::groups) {
     const int k0 = j * kTileKeys;
     cp_wait<0>();        // K_j
-    t.sync_group();      // ... of every thread; V and P of the tile before are no longer read
-    load_tile<D>(t.sv, D, vp + k0 * vs, vs, keys - k0, tid, kGroup);
+    sync_group();        // ... of every thread; V and P of the tile before are no longer read
+    load_tile<D>(sv, D, vp + k0 * vs, vs, keys - k0, tid, kGroup);
     cp_commit();
-    float2 s[4][8];
-    t.scores(s);
-    t.sync_group();      // K_j is no longer read
+    float2 s[4][8];   // (even, odd) head dims
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s[i][c] = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int d = 0; d < D; d += 4) {
+      float4 a[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (rg + 4 * i) * S::ld + d);
+#pragma unroll
+      for (int half = 0; half < 8; half += 4) {
+        float4 w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const float4*>(sk + (cg + 8 * (half + c)) * S::ld + d);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i][half + c] = __ffma2_rn(make_float2(a[i].x, a[i].y), make_float2(w[c].x, w[c].y), s[i][half + c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i][half + c] = __ffma2_rn(make_float2(a[i].z, a[i].w), make_float2(w[c].z, w[c].w), s[i][half + c]);
+      }
+    }
+    sync_group();        // K_j is no longer read
     constexpr int ahead = S::groups * kTileKeys;
-    if (j + S::groups < nt) load_tile<D>(t.sk, S::ld, kp + (int64_t)(k0 + ahead) * ks, ks, keys - k0 - ahead, tid, kGroup);
+    if (j + S::groups < nt) load_tile<D>(sk, S::ld, kp + (int64_t)(k0 + ahead) * ks, ks, keys - k0 - ahead, tid, kGroup);
     cp_commit();
-    t.weights(s, scale_log2, [&](int i) {
-      const int see = r0 + t.rg + 4 * i - k0;   // keys 0..see of the tile are visible to the row
-      return [see](int key) { return key <= see; };
-    });
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int see = r0 + rg + 4 * i - k0;   // keys 0..see of the tile are visible to the row
+      float x[8], mt = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        x[c] = cg + 8 * c <= see ? (s[i][c].x + s[i][c].y) * scale_log2 : -INFINITY;
+        mt = fmaxf(mt, x[c]);
+      }
+#pragma unroll
+      for (int w = 8; w > 1; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, w));   // the row's 8 threads
+      const float mn = fmaxf(m[i], mt), mu = mn == -INFINITY ? 0.f : mn;
+      const float corr = exp2f(m[i] - mu);
+      m[i] = mn;
+      float ps = 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float p = exp2f(x[c] - mu);
+        ps += p;
+        sp[(rg + 4 * i) * S::ldp + cg + 8 * c] = p;
+      }
+      l[i] = l[i] * corr + ps;
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        o[i][n].x *= corr;
+        o[i][n].y *= corr;
+        o[i][n].z *= corr;
+        o[i][n].w *= corr;
+      }
+    }
     cp_wait<1>();        // V_j
-    t.sync_group();      // ... and P_j
-    t.values();
+    sync_group();        // ... and P_j
+#pragma unroll 2
+    for (int k = 0; k < kTileKeys; k += 4) {
+      float p[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = *reinterpret_cast<const float4*>(sp + (rg + 4 * i) * S::ldp + k);
+        p[i][0] = x.x;
+        p[i][1] = x.y;
+        p[i][2] = x.z;
+        p[i][3] = x.w;
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          const float4 w = *reinterpret_cast<const float4*>(sv + (k + x) * D + 32 * n + 4 * cg);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 pp = make_float2(p[i][x], p[i][x]);
+            const float2 lo = __ffma2_rn(pp, make_float2(w.x, w.y), make_float2(o[i][n].x, o[i][n].y));
+            const float2 hi = __ffma2_rn(pp, make_float2(w.z, w.w), make_float2(o[i][n].z, o[i][n].w));
+            o[i][n] = make_float4(lo.x, lo.y, hi.x, hi.y);
+          }
+        }
+    }
   }
-  if (!t.join(smem, rows)) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int w = 8; w > 1; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+  // The other groups leave their maximum, sum and O where their tiles were; group 0 merges and stores.
+  if (group > 0) {
+    sync_group();        // the group's last tile is no longer read
+    float *so = sk, *sml = so + kTileRows * D;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = rg + 4 * i;
+      if (cg == 0) {
+        sml[2 * r] = m[i];
+        sml[2 * r + 1] = l[i];
+      }
+#pragma unroll
+      for (int n = 0; n < NC; ++n) *reinterpret_cast<float4*>(so + r * D + 32 * n + 4 * cg) = o[i][n];
+    }
+  }
+  cp_wait<0>();
+  __syncthreads();
+  if (group > 0) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = t.rg + 4 * i;
+    const int r = rg + 4 * i;
     if (r >= rows) continue;
-    const float inv = 1.f / t.l[i];
-    float* op = O + ((size_t)(c0 + r0 + r) * Hq + h) * D + 4 * t.cg;
+    // A row saw its own key at least, so its largest maximum is no -inf (unless it is no number).
+    float M = m[i];
+    for (int g = 1; g < S::groups; ++g) M = fmaxf(M, smem[S::k + g * S::per_group + kTileRows * D + 2 * r]);
+    float w = m[i] == M ? 1.f : exp2f(m[i] - M), sum = l[i] * w;
 #pragma unroll
-    for (int n = 0; n < Rows<D>::NC; ++n)
-      *reinterpret_cast<float4*>(op + 32 * n) = make_float4(t.o[i][n].x * inv, t.o[i][n].y * inv, t.o[i][n].z * inv, t.o[i][n].w * inv);
+    for (int n = 0; n < NC; ++n) o[i][n] = make_float4(o[i][n].x * w, o[i][n].y * w, o[i][n].z * w, o[i][n].w * w);
+    for (int g = 1; g < S::groups; ++g) {
+      const float* so = smem + S::k + g * S::per_group;
+      const float mg = so[kTileRows * D + 2 * r];
+      w = mg == M ? 1.f : exp2f(mg - M);
+      sum += so[kTileRows * D + 2 * r + 1] * w;
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        const float4 x = *reinterpret_cast<const float4*>(so + r * D + 32 * n + 4 * cg);
+        o[i][n] = make_float4(o[i][n].x + x.x * w, o[i][n].y + x.y * w, o[i][n].z + x.z * w, o[i][n].w + x.w * w);
+      }
+    }
+    const float inv = 1.f / sum;
+    float* op = O + ((size_t)(c0 + r0 + r) * Hq + h) * D + 4 * cg;
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+      *reinterpret_cast<float4*>(op + 32 * n) = make_float4(o[i][n].x * inv, o[i][n].y * inv, o[i][n].z * inv, o[i][n].w * inv);
   }
 }
 
