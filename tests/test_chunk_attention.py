@@ -406,7 +406,7 @@ def status(window_call=False, T=8, q_stride=None, q=4096, kp=4096, vp=4096, cu=4
 @pytest.mark.parametrize("window_call", [False, True])
 @pytest.mark.parametrize("kw,want", [
     (dict(T=-1), -1), (dict(q=0), -1), (dict(kp=0), -1), (dict(vp=0), -1), (dict(cu=0), -1), (dict(table=0), -1), (dict(o=0), -1),
-    (dict(q=4104), -1), (dict(kp=4098), -1), (dict(vp=4104), -1), (dict(o=4104), -1), (dict(ws=4112), -1),
+    (dict(q=4104), -1), (dict(kp=4098), -1), (dict(vp=4104), -1), (dict(o=4104), -1), (dict(ws=4112), -1), (dict(ws=0), -1),
     (dict(q_stride=511), -1), (dict(q_stride=516), -1), (dict(q_stride=-512), -1), (dict(dtype=F32, q_stride=514), -1),
     (dict(num=0), -1), (dict(P=64), -2), (dict(P=192), -2), (dict(P=384), -2), (dict(cap=1000), -2), (dict(P=0), -2),
     (dict(num=2 ** 30), -2), (dict(T=2 ** 30, cap=2 ** 20), -2), (dict(D=96), -2), (dict(Hkv=3), -2),
