@@ -448,7 +448,7 @@ MEDUSA_API int medusa_qk_norm_rotate(const medusa_cfg* cfg, const void* Q, const
  * it, from keys that other rows of the same call see.) A row all of whose visible
  * scores are -inf gives no number. O must not overlap an input. T = 0 enqueues nothing.
  * Alignment and q_stride as for medusa_prompt_attention; (num_pages + 1) * Hkv, or
- * (T / 8 + B) * Hq * (L_cap / 128 + 4), above 2^31 - 1 may be refused
+ * (T / 8 + 4 B) * Hq * (L_cap / 128 + 4), above 2^31 - 1 may be refused
  * (MEDUSA_ERR_UNSUPPORTED). The workspace has medusa_chunk_workspace_size()
  * bytes (256-byte aligned; NULL will do for 0) for T rows, which serve calls of fewer,
  * too; each call writes all of it that it reads, so calls one after the other may share it, and calls that may overlap
