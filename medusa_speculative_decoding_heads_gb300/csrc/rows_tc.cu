@@ -397,6 +397,11 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     // 24 single tokens 220 us.)
     const int t = warp - kPlanWarp;
     const ChunkSpace& sp = a.space;
+    // No cuts, ahead of every wait: the merge follows them even where one runs out and the rest is not reached.
+    if (lane == 0 && t == 0) {
+      if (sp.pair_streams) a.cuts[blockIdx.x] = ChunkCut{0, 0, 0, 0};
+      a.cuts[sp.pair_streams + blockIdx.x] = ChunkCut{0, 0, 0, 0};
+    }
     ChunkWalk<7> walk;
     {
       ChunkArgs c{};
@@ -419,7 +424,6 @@ rows_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     for (int single = sp.pair_streams ? 0 : 1; ok && single < 2; ++single) {
       const int log_npos = 7 - a.gp_shift;
       ChunkCut* cut_at = a.cuts + (single ? sp.pair_streams : 0) + blockIdx.x;
-      if (lane == 0 && t == 0) *cut_at = ChunkCut{0, 0, 0, 0};
       bool more = walk.open(single ? log_npos : log_npos + 1, single ? 1 : npos + 1, single ? npos : INT32_MAX,
                             single ? kSingleExtra : kPairExtra, (int)blockIdx.x, kSms);
       auto publish = [&](const ChunkPart& own, const ChunkPart& other, int dual) {   // own: this warp's tile's
