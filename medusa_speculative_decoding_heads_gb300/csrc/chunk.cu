@@ -20,10 +20,16 @@ constexpr int kMergeBlocks = 2;
 // 16); in float32, where little work is cut into many, up to thirty (D = 64: 15 and 10.6 us for five sequences).
 template <typename T, int D> constexpr int kMergeParts = sizeof(T) == 4 && D == 64 ? 4 : 2;
 
+// 2^x. In float32 as the attention kernel has it, down to 2^-149: a part 2^-130 below the row's maximum may still count.
+template <typename T>
 __device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+  if constexpr (sizeof(T) == 4) {
+    return exp2f(x);
+  } else {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+  }
 }
 
 // Row i of a cut: its parts turn, turn + step, ... by eight lanes, or by the four groups of eight of a warp.
@@ -68,7 +74,7 @@ __device__ __forceinline__ void join(const float* __restrict__ o_part, const flo
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       if (ml[i].x == -INFINITY && ml[i].y == 0.f) continue;   // nothing was visible: its O need not have been written
-      const float w = ex2(ml[i].x - mu);
+      const float w = ex2<T>(ml[i].x - mu);
       sum = fmaf(ml[i].y, w, sum);
 #pragma unroll
       for (int x = 0; x < X; ++x) {
