@@ -364,7 +364,8 @@ int medusa_qk_norm_rotate(const medusa_cfg* cfg, const void* Q, const void* K, i
     return MEDUSA_ERR_INVALID_ARG;
   if (ko_stride == 0 && ((int64_t)T != (int64_t)cfg->B * tree_shape(*cfg).N || Ko == K)) return MEDUSA_ERR_INVALID_ARG;
   if ((Qo == Q && qo_stride != q_stride) || (Ko == K && ko_stride != k_stride)) return MEDUSA_ERR_INVALID_ARG;
-  // blocks are counted in 32 bits (a token's heads go to Hq / 4 + Hkv / 4 + 2 groups at most, a group to 32 lanes at most)
+  // groups of heads are counted in 31 bits: four heads and more to each, and at most one group more for Hq and for Hkv (two
+  // heads to each only in calls of a few thousand heads in all)
   if ((int64_t)T * (cfg->Hq / 4 + cfg->Hkv / 4 + 2) > (int64_t)INT32_MAX) return MEDUSA_ERR_UNSUPPORTED;
   return from_cuda(launch_qk_norm_rotate(*cfg, Q, K, T, q_stride, k_stride, q_weight, k_weight, eps, inv_freq, rot_dim, pairing,
                                          pos, Qo, Ko, qo_stride, ko_stride, (cudaStream_t)stream));
