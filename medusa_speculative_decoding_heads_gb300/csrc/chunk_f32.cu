@@ -100,7 +100,7 @@ __device__ __forceinline__ void tile_unit(float* smem, const float* __restrict__
     t.sync_group();      // ... and P_j
     t.values();
   }
-  if (!t.join(smem, kTileRows)) return;
+  if (!t.join(smem)) return;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = t.rg + 4 * i;

@@ -10,7 +10,7 @@
 namespace medusa {
 namespace f32 {
 
-constexpr int kTileShift = 6, kTileRows = 1 << kTileShift, kTileKeys = 64, kGroup = 128;
+constexpr int kTileRows = 64, kTileKeys = 64, kGroup = 128;
 
 template <int D>
 struct Smem {
@@ -156,8 +156,8 @@ struct Rows {
         }
     }
   }
-  // The groups' results joined in group 0 (whose threads get true): m, l and o of rows [0, rows).
-  __device__ __forceinline__ bool join(float* smem, int rows) {
+  // The groups' results joined in group 0 (whose threads get true): m, l and o of the tile's rows.
+  __device__ __forceinline__ bool join(float* smem) {
     using S = Smem<D>;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -184,7 +184,6 @@ struct Rows {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = rg + 4 * i;
-      if (r >= rows) continue;
       float M = m[i];
       for (int g = 1; g < S::groups; ++g) M = fmaxf(M, smem[S::k + g * S::per_group + kTileRows * D + 2 * r]);
       // (a row's largest maximum is -inf only where it has seen nothing but -inf)
