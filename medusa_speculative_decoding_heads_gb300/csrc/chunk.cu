@@ -17,8 +17,10 @@ constexpr int kMergeThreads = 256, kMergeLanes = 8, kMergeRows = kMergeThreads /
 constexpr int kMergeSplit = 4;   // groups of lanes to a row of a single tile, whose parts they divide: there are few rows, of many parts
 constexpr int kMergeBlocks = 2;
 // Parts on their way at a time. In bf16 most rows have two or three (two: 12.6 us behind 2048 rows after 14336, four:
-// 16); in float32, where little work is cut into many, up to thirty (D = 64: 15 and 10.6 us for five sequences).
-template <typename T, int D> constexpr int kMergeParts = sizeof(T) == 4 && D == 64 ? 4 : 2;
+// 16); in float32, where little work is cut into many, up to thirty. Whole calls in float32 with four, and with two: one token
+// of 8000 rows, 8/4 heads, 17.3 and 18.0 us with D = 64, 18.9 and 19.4 with D = 128; five sequences of 0 to 700 rows 46.9 and 47.0,
+// 62.1 and 61.7; 24 tokens of 4000 rows, 32/8 heads of 128, 227 both.
+template <typename T> constexpr int kMergeParts = sizeof(T) == 4 ? 4 : 2;
 
 // 2^x. In float32 as the attention kernel has it, down to 2^-149: a part 2^-130 below the row's maximum may still count.
 template <typename T>
@@ -37,7 +39,7 @@ template <typename T, int D>
 __device__ __forceinline__ void join(const float* __restrict__ o_part, const float* __restrict__ ml_part, const ChunkSpace& sp,
                                      const ChunkCut& cut, bool pair, int stream, int i, int turn, int step, int sub, int Hq,
                                      T* __restrict__ O) {
-  constexpr int X = D / 32, P = kMergeParts<T, D>;
+  constexpr int X = D / 32, P = kMergeParts<T>;
   // rows of a tile lie [head][position]
   const int along = pair ? sp.npos : sp.single_npos, tile_rows = along << sp.gp_shift;
   const int tile = pair && i >= tile_rows, in_tile = i - tile * tile_rows;
