@@ -336,8 +336,8 @@ MEDUSA_API int medusa_tree_attention_noalloc(const medusa_cfg* cfg, const void* 
  * the product with V. Rows of O that no sequence owns are left as they are.
  * cu_rows must not decrease: a sequence with cu_rows[b+1] < cu_rows[b] and all
  * behind it are skipped. A sequence with cu_rows[b] < 0 or cu_rows[b+1] > T is
- * skipped, too. Non-finite values stay within their own sequence (there, a value
- * of V that is no number may reach earlier rows too). O must not overlap Q, K or V. T = 0 enqueues nothing. From cfg only
+ * skipped, too. Non-finite values stay within their own sequence (there, a value of V that
+ * is infinite or no number may reach earlier rows too). O must not overlap Q, K or V. T = 0 enqueues nothing. From cfg only
  * B, Hq, Hkv, D and dtype are used (every prompt length is allowed, whatever
  * L_cap), but all of it is checked. Q, K, V, O 16-byte aligned; strides multiples
  * of 16 bytes and at least Hq * D (Hkv * D): MEDUSA_ERR_INVALID_ARG otherwise.
@@ -380,7 +380,7 @@ MEDUSA_API int medusa_kv_store_paged(const medusa_cfg* cfg, const void* K, const
  * rows per sequence and takes its own rows by itself). A row all of whose visible
  * scores are -inf gives zeros. Rows past L_b in a sequence's own pages, and
  * shared rows past the longest length, never reach a result, whatever they hold.
- * A key that a row does not see never reaches it. (A value that is no number may:
+ * A key that a row does not see never reaches it. (A value that is infinite or no number may:
  * from a shared row that another sequence has, or from a staged row of the same
  * sequence. Its weight is 0, the product is not.) bf16 with D = 128 only, and at most 2^31 - 1
  * query rows and page planes (MEDUSA_ERR_UNSUPPORTED otherwise). The workspace has
@@ -439,13 +439,16 @@ MEDUSA_API int medusa_qk_norm_rotate(const medusa_cfg* cfg, const void* Q, const
  *                              softmax over logical rows 0..p of q.k / sqrt(D),
  *                              times v; KV head of query head h is h / (Hq / Hkv)
  * Softmax and accumulation in float32; bf16 weights are rounded to bf16 before
- * the product with V. Rows of O that no sequence owns are left as they are, and so
+ * the product with V, and one below 2^-118 of a row's largest may count as none. What is
+ * summed goes by the largest score of a part of the keys: |V| summed over the rows that a
+ * row sees has to stay below 2^127 (bf16: 2^119), or the row may give no number.
+ * Rows of O that no sequence owns are left as they are, and so
  * are those of a sequence that is skipped: cu_rows as for medusa_prompt_attention,
  * or start[b] < 0, or start[b] + its rows > L_cap. Block-table entries past a
  * sequence's last page are not read; a page id outside [0, num_pages) stands for
  * rows of zeros. Cache rows that no row of a sequence sees may hold anything. (Among
- * rows of one sequence, a value of V that is no number may reach rows that do not see
- * it, from keys that other rows of the same call see.) A row all of whose visible
+ * rows of one sequence, a value of V that is infinite or no number may reach rows that do
+ * not see it, from keys that other rows of the same call see.) A row all of whose visible
  * scores are -inf gives no number. O must not overlap an input. T = 0 enqueues nothing.
  * Alignment and q_stride as for medusa_prompt_attention; (num_pages + 1) * Hkv, or
  * (T / 8 + 4 B) * Hq * (L_cap / 128 + 4), above 2^31 - 1 may be refused
