@@ -2,7 +2,7 @@
 //
 // y = x w / sqrt(mean(x^2) + eps); then pairs (y_u, y_v) of the first R head dims turn by the angle
 // a = pos f_i: (y_u cos a - y_v sin a, y_v cos a + y_u sin a). Bound by the bytes of Q and K, read
-// once and written once: 8191 tokens of 40/40 heads in bf16 59.4 us (5.65 TB/s, 0.83 of the measured copy).
+// once and written once: 8191 tokens of 40/40 heads in bf16 59.4 to 60.1 us (5.6 TB/s, 0.83 of the measured copy).
 //
 // D / 8 lanes hold a head, 8 head dims each, in two pieces of 4 that lie so that both dims of a pair
 // are in the same lane: R / 2 apart where halves turn against each other, next to each other where

@@ -19,7 +19,11 @@
 //                   The product with V begins once half of the weights are there. (bf16 is what
 //                   the matrix instruction takes beside a bf16 V: each weight is off by 2^-8 of itself at
 //                   most, an output by 2^-8 of its weights times |v|. Against 64 bits, relative: 0.0020 to
-//                   0.0023 on the cases measured, and 0.0016 for float32 rounded once at the end.)
+//                   0.0023 on the cases measured, and 0.0016 for float32 rounded once at the end. Weights as two bf16
+//                   values, each multiplied with V, come to the 0.0016; new tokens over a paged cache took, so and as
+//                   they are: 2048 rows after 14336 488 and 348 us, 8192 rows in a window of 1024 243 and 158, 24 single
+//                   tokens 150 and 124, 32 of 4096 to 16384 rows 205 and 194. With the second product for single tokens
+//                   alone, a branch in the softmax, all of them lost: 384, 212, 167 and 215.)
 //   warp 8          issues every MMA: S_t(j) = Q_t K_j^T (both operands in shared memory)
 //                   and O_t += P_t(j) V_j (P from TMEM), so that one tile's products run
 //                   while the other tile's softmax does. MMAs of one issuing thread run in
@@ -32,9 +36,9 @@
 //                   unit while the others work on this one.
 // New tokens over a paged cache (kChunkMode) differ in the schedule, in where K and V lie and in masks: one
 // CTA per SM has its range of all key tiles (chunk.cuh), which warps 10 and 11 follow, a tile's half each; warp 9
-// puts off what it would have to wait for. 2048 rows after 14336, 32/8 heads: 308 us alone between pauses (1670
-// TFLOP/s, 0.87 of the measured cuBLAS burst), 340 with the merge in a loop under the power limit; 32 single tokens
-// of 4096 to 16384 rows 194 us (6.7 TB/s, 0.98 of the measured copy).
+// puts off what it would have to wait for. 2048 rows after 14336, 32/8 heads: 311 us launched by itself (1660
+// TFLOP/s, 0.87 of the measured cuBLAS burst), 342 to 348 with the merge in a loop under the power limit; 32 single tokens
+// of 4096 to 16384 rows 192 to 194 us (6.7 TB/s, 0.98 of the measured copy).
 // TMEM: S_0, S_1, O_0, O_1 (128 columns each; O uses D of them). Every mbarrier wait is bounded.
 #include <cuda.h>
 #include <cudaTypedefs.h>
