@@ -36,8 +36,8 @@
 //                   unit while the others work on this one.
 // New tokens over a paged cache (kChunkMode) differ in the schedule, in where K and V lie and in masks: one
 // CTA per SM has its range of all key tiles (chunk.cuh), which warps 10 and 11 follow, a tile's half each; warp 9
-// puts off what it would have to wait for. 2048 rows after 14336, 32/8 heads: 311 us launched by itself (1660
-// TFLOP/s, 0.87 of the measured cuBLAS burst), 342 to 348 with the merge in a loop under the power limit; 32 single tokens
+// puts off what it would have to wait for. 2048 rows after 14336, 32/8 heads: 310 us launched by itself (1660
+// TFLOP/s, 0.87 of the measured cuBLAS burst), 341 to 348 with the merge in a loop under the power limit; 32 single tokens
 // of 4096 to 16384 rows 192 to 194 us (6.7 TB/s, 0.98 of the measured copy).
 // TMEM: S_0, S_1, O_0, O_1 (128 columns each; O uses D of them). Every mbarrier wait is bounded.
 #include <cuda.h>
