@@ -439,7 +439,7 @@ MEDUSA_API int medusa_qk_norm_rotate(const medusa_cfg* cfg, const void* Q, const
  *                              softmax over logical rows 0..p of q.k / sqrt(D),
  *                              times v; KV head of query head h is h / (Hq / Hkv)
  * Softmax and accumulation in float32; bf16 weights are rounded to bf16 before
- * the product with V, and one below 2^-118 of a row's largest may count as none. What is
+ * the product with V, and one below 2^-110 of a row's largest may count as none. What is
  * summed goes by the largest score of a part of the keys: |V| summed over the rows that a
  * row sees has to stay below 2^127 (bf16: 2^119), or the row may give no number.
  * Rows of O that no sequence owns are left as they are, and so
